@@ -15,6 +15,8 @@ The operators (see the header for the exact definitions):
 * ``dit_swiglu``           silu(a) * b
 * ``dit_gated_residual_adaln``  res = x + gate_b * y, then LN(res) * (1 + scale_b) + shift_b
 * ``dit_frames_to_u8``     decoded fp32 frames [B, C, T, H, W] -> uint8 BTHWC (or planar BTCHW)
+* ``dit_qk_rope_scaled``, ``dit_qkv_rope_append``, ``dit_paged_attention``  chunks of new tokens
+  over a paged key/value cache (``paged.py``, ``include/dit_paged.h``)
 
 All run over a packed sequence described by ``cu_seqlens`` (cumulative valid
 lengths) and ``cu_seqlens_padded`` (row offsets), touching valid rows only.
@@ -29,7 +31,8 @@ import torch
 
 __all__ = ["dit_qk_rmsnorm_rope", "dit_adaln_modulate", "dit_gated_residual", "dit_swiglu",
            "dit_gated_residual_adaln", "dit_frames_to_u8",
-           "dit_validate_seqlens", "check_seqlens", "DitError", "library", "LIB_PATH", "STATUS"]
+           "dit_rope_frequencies", "dit_qk_rope_scaled", "dit_qkv_rope_append", "dit_paged_attention",
+           "dit_paged_attention_workspace", "dit_validate_seqlens", "check_seqlens", "DitError", "library", "LIB_PATH", "STATUS"]
 
 # DIT_TOKEN_LIB may point at another build of the same library.
 LIB_PATH = os.environ.get("DIT_TOKEN_LIB") or os.path.join(os.path.dirname(os.path.abspath(__file__)),
@@ -51,6 +54,7 @@ _VP = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 
 _SIGNATURES = {
     "dit_qk_rmsnorm_rope": [_VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I32, _I64, _I32, _I32, _I32,
@@ -73,6 +77,15 @@ _SIGNATURES = {
     "dit_validate_seqlens": [_VP, _VP, _I32, _I64, _VP, _VP],
     "dit_av_stream_seqlens": [_VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP],
     "dit_frames_to_u8": [_VP, _I64, _I64, _I64, _I64, _I64, _I32, _VP, _VP],
+    "dit_rope_frequencies": [_I32, _F64, _I32, _F64, _I64, _F64, _F64, _VP, _VP],
+    "dit_qk_rope_scaled": [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I32, _I64, _I32, _I32,
+                           _I32, _VP, _I32, _VP, _VP, _I32, _I32, _I32, _VP, _F32, _F32, _I32, _VP],
+    "dit_qkv_rope_append": [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _I32,
+                            _I32, _VP, _I64, _I32, _VP, _VP, _VP, _I32, _I64, _I32, _I32, _I32, _VP, _I32, _VP, _VP,
+                            _I32, _I32, _I32, _VP, _F32, _F32, _I32, _VP],
+    "dit_paged_attention": [_VP, _I64, _VP, _VP, _I64, _I64, _I64, _I32, _I32, _VP, _I64, _I32, _VP, _VP, _VP, _I32,
+                            _I64, _I32, _I32, _I32, _F32, _I32, _I32, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP],
+    "dit_paged_attention_workspace": [_I64, _I32, _I32, _I32, _I32, _I64, _I64, _VP],
     "dit_status_string": [_I32],
     "dit_last_cuda_error": [],
     "dit_abi_version": [],
@@ -377,3 +390,7 @@ def check_seqlens(cu_seqlens: torch.Tensor, cu_seqlens_padded: torch.Tensor, num
     if bad:
         raise DitError("dit_validate_seqlens", 5,
                        f"{library().dit_status_string(5).decode()}: first bad sequence {first}")
+
+
+from .paged import (dit_paged_attention, dit_paged_attention_workspace, dit_qk_rope_scaled,  # noqa: E402
+                    dit_qkv_rope_append, dit_rope_frequencies)

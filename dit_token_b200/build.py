@@ -3,8 +3,8 @@
     python -m dit_token_b200.build [--force] [--verbose]
     python -m dit_token_b200.build --define DIT_PDL=0 --out PATH.so
 
-nvcc compiles every csrc/*.cu for sm_100a (cross-compiles without a GPU) and
-links them into one shared library with the CUDA runtime linked statically,
+nvcc compiles every csrc/*.cu for sm_100a (cross-compiles without a GPU, the
+files side by side) and links them into one shared library with the CUDA runtime linked statically,
 so loading the library needs no GPU and no libcudart on the search path.
 A build with compile-time switches (``--define``, e.g. DIT_PDL=0: launches
 without programmatic dependent launch) goes to its own file, never over the
@@ -16,6 +16,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -38,7 +40,7 @@ def sources():
 
 def _deps():
     return sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))) + \
-        [os.path.join(INCLUDE, "dit_token.h"), os.path.abspath(__file__)]
+        sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
@@ -56,12 +58,18 @@ def build(force: bool = False, verbose: bool = False, out: str = None, defines=(
     tmp = f"{target}.{os.getpid()}.tmp"  # per process: concurrent builds never share a file
     # Exported symbols: only the extern "C" entry points (default visibility is
     # hidden for everything else, see -fvisibility=hidden and the header).
-    cmd = [NVCC, *NVCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, "-I", CSRC, "-shared", "-o", tmp,
-           *sources()]
+    flags = [*NVCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, "-I", CSRC]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.check_call(cmd)
+        flags.insert(0, "-Xptxas=-v")
+    with tempfile.TemporaryDirectory() as objs, ThreadPoolExecutor(max(1, min(8, os.cpu_count() or 1))) as pool:
+        def compile_one(src):
+            obj = os.path.join(objs, os.path.basename(src) + ".o")
+            cmd = [NVCC, *flags, "-c", "-o", obj, src]
+            if verbose:
+                print(" ".join(cmd))
+            subprocess.check_call(cmd)
+            return obj
+        subprocess.check_call([NVCC, *NVCC_FLAGS, "-shared", "-o", tmp, *pool.map(compile_one, sources())])
     os.replace(tmp, target)
     return target
 

@@ -1,4 +1,4 @@
-// api.cu -- the C ABI declared in include/dit_token.h: host-side argument
+// api.cu -- the C ABI declared in include/dit_token.h and dit_paged.h: host-side argument
 // checks, the rotary frequency bases, and the launches.  Nothing here
 // allocates or synchronizes; the only state is thread-local: the last CUDA
 // error.
@@ -7,6 +7,7 @@
 
 #include <cuda_runtime.h>
 
+#include "dit_paged.h"
 #include "dit_token.h"
 #include "launch.h"
 
@@ -73,6 +74,56 @@ dit_status check_packing(const int32_t* cs, const int32_t* cp, int32_t num_seqs,
 dit::Packing packing(const int32_t* cs, const int32_t* cp, int32_t num_seqs, int64_t num_rows_padded)
 {
     return dit::Packing{cs, cp, num_seqs, (int32_t)num_rows_padded};
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Checks shared by the two calls that turn q and k by a frequency table.
+dit_status check_rope_table(int32_t num_q_heads, int32_t num_k_heads, int32_t head_dim, int32_t rotary_dim,
+                            const int32_t* rope_grid, int32_t sec_t, int32_t sec_h, int32_t sec_w, float attn_scale,
+                            float eps, int32_t rope_mode)
+{
+    if (num_q_heads < 0 || num_k_heads < 0 || head_dim <= 0)
+        return DIT_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+        return DIT_ERR_UNSUPPORTED;
+    if (rope_mode != DIT_ROPE_INTERLEAVED && rope_mode != DIT_ROPE_HALF && rope_mode != DIT_ROPE_NONE)
+        return DIT_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f) || !std::isfinite(eps) || !std::isfinite(attn_scale))
+        return DIT_ERR_SHAPE;
+    if (rope_mode == DIT_ROPE_NONE)
+        return DIT_OK;
+    if (rotary_dim < 8 || rotary_dim > head_dim || (rotary_dim & 7))
+        return DIT_ERR_SHAPE;
+    if (rope_grid && (sec_t < 0 || sec_h < 0 || sec_w < 0 || (sec_t | sec_h | sec_w) & 1 ||
+                      (int64_t)sec_t + sec_h + sec_w != rotary_dim))
+        return DIT_ERR_SHAPE;
+    return DIT_OK;
+}
+
+// The cache's sizes and strides.
+dit_status check_cache(int32_t head_dim, int64_t page_stride, int64_t slot_stride, int64_t head_stride,
+                       int32_t num_pages, int32_t page_size, int64_t table_stride, int32_t max_pages)
+{
+    if (num_pages < 0 || page_size <= 0 || max_pages < 0 || table_stride < max_pages || page_stride < 0 ||
+        slot_stride < head_dim || head_stride < head_dim)
+        return DIT_ERR_SHAPE;
+    if (!mult8(page_stride) || !mult8(slot_stride) || !mult8(head_stride))
+        return DIT_ERR_ALIGN;
+    return DIT_OK;
+}
+
+void set_rope_table(dit::RopeCacheParams& p, const double* freqs, const double* grid_freqs, int32_t rotary_dim,
+                    const int32_t* rope_grid, const int32_t* pos_offset, int32_t sec_t, int32_t sec_h, int32_t rope_mode)
+{
+    const bool turns = rope_mode != DIT_ROPE_NONE;
+    p.freqs = freqs;
+    p.grid_freqs = grid_freqs;
+    p.rotary_dim = turns ? rotary_dim : 0;
+    p.rope_grid = turns ? rope_grid : nullptr;
+    p.pos_offset = pos_offset;
+    p.sec_pairs[0] = sec_t / 2;
+    p.sec_pairs[1] = sec_h / 2;
 }
 
 }  // namespace
@@ -376,6 +427,273 @@ dit_status dit_av_stream_seqlens(const int32_t* cu_seqlens, const int32_t* cu_se
     return from_cuda(dit::launch_av_stream_seqlens(cu_seqlens, cu_seqlens_padded, rope_grid, pos_offset, num_seqs,
                                                    out_cu_seqlens, out_cu_seqlens_padded,
                                                    static_cast<cudaStream_t>(stream)));
+}
+
+dit_status dit_rope_frequencies(int32_t rotary_dim, double theta, int32_t scaling, double factor,
+                                int64_t original_len, double beta_fast, double beta_slow, double* freqs,
+                                float* attn_scale)
+{
+    if (rotary_dim <= 0 || (rotary_dim & 1) || !(theta > 0.0) || !std::isfinite(theta))
+        return DIT_ERR_SHAPE;
+    if (scaling < DIT_ROPE_SCALE_NONE || scaling > DIT_ROPE_SCALE_YARN)
+        return DIT_ERR_UNSUPPORTED;
+    if (scaling != DIT_ROPE_SCALE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+        return DIT_ERR_SHAPE;
+    if (scaling == DIT_ROPE_SCALE_YARN &&
+        (original_len <= 0 || !(theta > 1.0) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
+         !std::isfinite(beta_fast)))
+        return DIT_ERR_SHAPE;
+    if (!freqs || !attn_scale)
+        return DIT_ERR_NULL;
+    const double R = rotary_dim;
+    double base = theta, lo = 0.0, hi = 0.0;
+    if (scaling == DIT_ROPE_SCALE_NTK && rotary_dim > 2)
+        base = theta * std::pow(factor, R / (R - 2.0));
+    if (scaling == DIT_ROPE_SCALE_YARN) {
+        constexpr double kTwoPi = 6.283185307179586476925286766559;
+        auto pair_at = [&](double turns) {
+            return R * std::log((double)original_len / (kTwoPi * turns)) / (2.0 * std::log(theta));
+        };
+        lo = std::fmax(std::floor(pair_at(beta_fast)), 0.0);
+        hi = std::fmin(std::ceil(pair_at(beta_slow)), R - 1.0);
+    }
+    for (int32_t j = 0; j < rotary_dim / 2; ++j) {
+        double f = std::pow(base, -2.0 * j / R);
+        if (scaling == DIT_ROPE_SCALE_LINEAR)
+            f /= factor;
+        if (scaling == DIT_ROPE_SCALE_YARN) {
+            const double r = std::fmin(std::fmax((j - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+            f = f / factor * r + f * (1.0 - r);
+        }
+        freqs[j] = f;
+    }
+    *attn_scale = scaling == DIT_ROPE_SCALE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+    return DIT_OK;
+}
+
+dit_status dit_qk_rope_scaled(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, void* q_out,
+                              int64_t q_out_stride, void* k_out, int64_t k_out_stride, const void* q_weight,
+                              const void* k_weight, const int32_t* cu_seqlens, const int32_t* cu_seqlens_padded,
+                              int32_t num_seqs, int64_t num_rows_padded, int32_t num_q_heads, int32_t num_k_heads,
+                              int32_t head_dim, const double* freqs, int32_t rotary_dim, const int32_t* rope_grid,
+                              const double* grid_freqs, int32_t sec_t, int32_t sec_h, int32_t sec_w,
+                              const int32_t* pos_offset, float attn_scale, float eps, int32_t rope_mode, void* stream)
+{
+    bool empty = false;
+    dit_status st = check_packing(cu_seqlens, cu_seqlens_padded, num_seqs, num_rows_padded, &empty);
+    if (st != DIT_OK)
+        return st;
+    st = check_rope_table(num_q_heads, num_k_heads, head_dim, rotary_dim, rope_grid, sec_t, sec_h, sec_w, attn_scale,
+                          eps, rope_mode);
+    if (st != DIT_OK)
+        return st;
+    if (!q_out)
+        q_out_stride = q_row_stride;
+    if (!k_out)
+        k_out_stride = k_row_stride;
+    const int64_t qw = (int64_t)num_q_heads * head_dim, kw = (int64_t)num_k_heads * head_dim;
+    if (q_row_stride < qw || q_out_stride < qw || k_row_stride < kw || k_out_stride < kw)
+        return DIT_ERR_SHAPE;
+    if (empty || num_q_heads + num_k_heads == 0)
+        return DIT_OK;
+    const bool turns = rope_mode != DIT_ROPE_NONE;
+    if ((num_q_heads > 0 && !q) || (num_k_heads > 0 && !k) || (q_weight == nullptr) != (k_weight == nullptr) ||
+        (turns && !freqs) || (turns && rope_grid && !grid_freqs))
+        return DIT_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(q_weight) ||
+        !aligned16(k_weight) || !aligned16(freqs) || !aligned16(grid_freqs) || !mult8(q_row_stride) ||
+        !mult8(k_row_stride) || !mult8(q_out_stride) || !mult8(k_out_stride) || !aligned4(rope_grid) ||
+        !aligned4(pos_offset))
+        return DIT_ERR_ALIGN;
+    dit::RopeCacheParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.q_out = static_cast<uint16_t*>(q_out ? q_out : const_cast<void*>(q));
+    p.k_out = static_cast<uint16_t*>(k_out ? k_out : const_cast<void*>(k));
+    p.q_weight = static_cast<const uint16_t*>(q_weight);
+    p.k_weight = static_cast<const uint16_t*>(k_weight);
+    p.q_row_stride = q_row_stride;
+    p.k_row_stride = k_row_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.pk = packing(cu_seqlens, cu_seqlens_padded, num_seqs, num_rows_padded);
+    p.num_q_heads = num_q_heads;
+    p.num_k_heads = num_k_heads;
+    p.eps = eps;
+    p.attn_scale = attn_scale;
+    set_rope_table(p, freqs, grid_freqs, rotary_dim, rope_grid, pos_offset, sec_t, sec_h, rope_mode);
+    return from_cuda(dit::launch_rope_cache(p, head_dim, rope_mode, static_cast<cudaStream_t>(stream)));
+}
+
+dit_status dit_qkv_rope_append(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                               const void* v, int64_t v_row_stride, void* q_out, int64_t q_out_stride,
+                               const void* q_weight, const void* k_weight, void* k_cache, void* v_cache,
+                               int64_t page_stride, int64_t slot_stride, int64_t head_stride, int32_t num_pages,
+                               int32_t page_size, const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                               const int32_t* cache_lens, const int32_t* cu_seqlens, const int32_t* cu_seqlens_padded,
+                               int32_t num_seqs, int64_t num_rows_padded, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, const double* freqs, int32_t rotary_dim, const int32_t* rope_grid,
+                               const double* grid_freqs, int32_t sec_t, int32_t sec_h, int32_t sec_w,
+                               const int32_t* pos_offset, float attn_scale, float eps, int32_t rope_mode, void* stream)
+{
+    bool empty = false;
+    dit_status st = check_packing(cu_seqlens, cu_seqlens_padded, num_seqs, num_rows_padded, &empty);
+    if (st != DIT_OK)
+        return st;
+    st = check_rope_table(num_q_heads, num_kv_heads, head_dim, rotary_dim, rope_grid, sec_t, sec_h, sec_w, attn_scale,
+                          eps, rope_mode);
+    if (st != DIT_OK)
+        return st;
+    if (!q_out)
+        q_out_stride = q_row_stride;
+    const int64_t qw = (int64_t)num_q_heads * head_dim, kw = (int64_t)num_kv_heads * head_dim;
+    if (num_kv_heads <= 0 || q_row_stride < qw || q_out_stride < qw || k_row_stride < kw || v_row_stride < kw)
+        return DIT_ERR_SHAPE;
+    st = check_cache(head_dim, page_stride, slot_stride, head_stride, num_pages, page_size, table_stride, max_pages);
+    if (st != DIT_OK)
+        return st;
+    if (empty)
+        return DIT_OK;
+    const bool turns = rope_mode != DIT_ROPE_NONE;
+    if ((num_q_heads > 0 && !q) || !k || !v || (q_weight == nullptr) != (k_weight == nullptr) || !k_cache ||
+        !v_cache || !block_table || !cache_lens || (turns && !freqs) || (turns && rope_grid && !grid_freqs))
+        return DIT_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(q_weight) ||
+        !aligned16(k_weight) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(freqs) ||
+        !aligned16(grid_freqs) || !mult8(q_row_stride) || !mult8(k_row_stride) || !mult8(v_row_stride) ||
+        !mult8(q_out_stride) || !aligned4(rope_grid) || !aligned4(pos_offset) || !aligned4(block_table) ||
+        !aligned4(cache_lens))
+        return DIT_ERR_ALIGN;
+    dit::RopeCacheParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.q_out = static_cast<uint16_t*>(q_out ? q_out : const_cast<void*>(q));
+    p.k_cache = static_cast<uint16_t*>(k_cache);
+    p.v_cache = static_cast<uint16_t*>(v_cache);
+    p.q_weight = static_cast<const uint16_t*>(q_weight);
+    p.k_weight = static_cast<const uint16_t*>(k_weight);
+    p.block_table = block_table;
+    p.cache_lens = cache_lens;
+    p.q_row_stride = q_row_stride;
+    p.k_row_stride = k_row_stride;
+    p.v_row_stride = v_row_stride;
+    p.q_out_stride = q_out_stride;
+    p.page_stride = page_stride;
+    p.slot_stride = slot_stride;
+    p.head_stride = head_stride;
+    p.table_stride = table_stride;
+    p.pk = packing(cu_seqlens, cu_seqlens_padded, num_seqs, num_rows_padded);
+    p.num_q_heads = num_q_heads;
+    p.num_k_heads = num_kv_heads;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.eps = eps;
+    p.attn_scale = attn_scale;
+    set_rope_table(p, freqs, grid_freqs, rotary_dim, rope_grid, pos_offset, sec_t, sec_h, rope_mode);
+    return from_cuda(dit::launch_rope_cache(p, head_dim, rope_mode, static_cast<cudaStream_t>(stream)));
+}
+
+dit_status dit_paged_attention_workspace(int64_t num_rows_padded, int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t num_kv_heads, int32_t head_dim, int64_t max_chunk,
+                                         int64_t max_kv_len, int64_t* bytes)
+{
+    if (num_seqs < 0 || num_rows_padded < 0 || num_rows_padded > INT32_MAX || num_q_heads <= 0 || num_kv_heads <= 0 ||
+        num_q_heads % num_kv_heads != 0 || max_kv_len <= 0 || max_kv_len > INT32_MAX || head_dim <= 0)
+        return DIT_ERR_SHAPE;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || num_kv_heads > dit::kMaxKvHeads)
+        return DIT_ERR_UNSUPPORTED;
+    if (!bytes)
+        return DIT_ERR_NULL;
+    *bytes = 0;
+    if (num_seqs == 0 || num_rows_padded == 0)
+        return DIT_OK;
+    dit::PagedPlan plan{};
+    if (!dit::paged_plan(num_rows_padded, num_seqs, num_q_heads, num_kv_heads, head_dim, max_chunk, max_kv_len, 0, plan))
+        return DIT_ERR_SHAPE;
+    *bytes = plan.most_bytes;
+    return DIT_OK;
+}
+
+dit_status dit_paged_attention(const void* q, int64_t q_row_stride, const void* k_cache, const void* v_cache,
+                               int64_t page_stride, int64_t slot_stride, int64_t head_stride, int32_t num_pages,
+                               int32_t page_size, const int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                               const int32_t* kv_lens, const int32_t* cu_seqlens, const int32_t* cu_seqlens_padded,
+                               int32_t num_seqs, int64_t num_rows_padded, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, float softmax_scale, int32_t causal, int32_t window,
+                               int64_t max_chunk, int64_t max_kv_len, void* out, int64_t out_row_stride, float* lse,
+                               void* workspace, int64_t workspace_bytes, void* stream)
+{
+    bool empty = false;
+    dit_status st = check_packing(cu_seqlens, cu_seqlens_padded, num_seqs, num_rows_padded, &empty);
+    if (st != DIT_OK)
+        return st;
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || head_dim <= 0 ||
+        !(softmax_scale > 0.f) || !std::isfinite(softmax_scale) || window < 0 || workspace_bytes < 0 ||
+        q_row_stride < (int64_t)num_q_heads * head_dim || out_row_stride < (int64_t)num_q_heads * head_dim)
+        return DIT_ERR_SHAPE;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || num_kv_heads > dit::kMaxKvHeads)
+        return DIT_ERR_UNSUPPORTED;
+    st = check_cache(head_dim, page_stride, slot_stride, head_stride, num_pages, page_size, table_stride, max_pages);
+    if (st != DIT_OK)
+        return st;
+    if (empty)
+        return DIT_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !kv_lens || !out)
+        return DIT_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
+        !mult8(q_row_stride) || !mult8(out_row_stride) || !aligned4(block_table) || !aligned4(kv_lens) ||
+        !aligned4(lse))
+        return DIT_ERR_ALIGN;
+    const int64_t capacity = (int64_t)max_pages * page_size;
+    int64_t keys = max_kv_len > 0 && max_kv_len < capacity ? max_kv_len : capacity;
+    keys = keys < 1 ? 1 : (keys > INT32_MAX ? INT32_MAX : keys);
+    dit::PagedPlan plan{};
+    if (!dit::paged_plan(num_rows_padded, num_seqs, num_q_heads, num_kv_heads, head_dim, max_chunk, keys, window, plan))
+        return DIT_ERR_SHAPE;
+    if (plan.bytes > workspace_bytes)
+        return DIT_ERR_SHAPE;
+    if (plan.bytes > 0 && !workspace)
+        return DIT_ERR_NULL;
+    dit::PagedParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k_cache = static_cast<const uint16_t*>(k_cache);
+    p.v_cache = static_cast<const uint16_t*>(v_cache);
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.block_table = block_table;
+    p.kv_lens = kv_lens;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
+                                          num_rows_padded * num_q_heads * plan.splits * head_dim * 4);
+    p.q_row_stride = q_row_stride;
+    p.out_row_stride = out_row_stride;
+    p.page_stride = page_stride;
+    p.slot_stride = slot_stride;
+    p.head_stride = head_stride;
+    p.table_stride = table_stride;
+    p.pk = packing(cu_seqlens, cu_seqlens_padded, num_seqs, num_rows_padded);
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    // key / page_size = key * ceil(2^s / page_size) >> s with 2^(s - 31) >= page_size:
+    // exact for keys below 2^31
+    uint32_t log2_up = 0;
+    while ((1ull << log2_up) < (uint64_t)page_size)
+        ++log2_up;
+    p.page_shift = 31 + log2_up;
+    p.page_mul = (uint32_t)(((1ull << p.page_shift) + (uint64_t)page_size - 1) / (uint64_t)page_size);
+    constexpr float kLog2e = 1.4426950408889634f;
+    p.scale_log2 = softmax_scale * kLog2e;
+    p.causal = causal != 0;
+    p.window = window;
+    p.splits = plan.splits;
+    p.split_keys = plan.split_keys;
+    return from_cuda(dit::launch_paged_attention(p, plan, head_dim, static_cast<cudaStream_t>(stream)));
 }
 
 const char* dit_status_string(dit_status s)

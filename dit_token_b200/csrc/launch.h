@@ -145,6 +145,78 @@ struct FramesParams {
     int32_t layout;
 };
 
+// dit_qk_rope_scaled (block_table null: k goes to k_out, no v) and
+// dit_qkv_rope_append (k and v go to the cache).  Without rotation
+// rotary_dim is 0 and every lane passes.
+struct RopeCacheParams {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;  // null: none
+    uint16_t* q_out;
+    uint16_t* k_out;
+    uint16_t* k_cache;
+    uint16_t* v_cache;
+    const uint16_t* q_weight;  // both null: no RMSNorm
+    const uint16_t* k_weight;
+    const double* freqs;       // [rotary_dim / 2] pair frequencies of 1D rows
+    const double* grid_freqs;  // [rotary_dim / 2] of 3D rows, t, h, w pairs in order
+    const int32_t* rope_grid;
+    const int32_t* pos_offset;
+    const int32_t* block_table;
+    const int32_t* cache_lens;
+    int64_t q_row_stride, k_row_stride, v_row_stride, q_out_stride, k_out_stride;
+    int64_t page_stride, slot_stride, head_stride;
+    int64_t table_stride;
+    Packing pk;
+    int32_t num_q_heads, num_k_heads;
+    int32_t rotary_dim;
+    int32_t sec_pairs[2];  // pairs of the t and h sections
+    int32_t num_pages, page_size, max_pages;
+    float eps, attn_scale;
+    int32_t runs_per_row, batches_per_run;  // set by the launcher
+};
+
+// dit_paged_attention.
+struct PagedParams {
+    const uint16_t* q;
+    const uint16_t* k_cache;
+    const uint16_t* v_cache;
+    uint16_t* out;
+    float* lse;  // [num_rows_padded][num_q_heads] or null
+    const int32_t* block_table;
+    const int32_t* kv_lens;
+    float* part_o;    // partial sums of the splits, see partial_index
+    float2* part_ml;
+    int64_t q_row_stride, out_row_stride;
+    int64_t page_stride, slot_stride, head_stride;
+    int64_t table_stride;
+    Packing pk;
+    int32_t num_q_heads, num_kv_heads, group;  // group = q heads per key head
+    int32_t num_pages, page_size, max_pages;
+    uint32_t page_mul, page_shift;  // key / page_size = key * page_mul >> page_shift
+    float scale_log2;               // softmax scale times log2(e)
+    int32_t causal, window;         // window 0: none
+    int32_t splits, split_keys;
+};
+
+// Which kernel a call takes, and how the key axis is cut.
+constexpr int kPagedNarrow = 0;
+constexpr int kPagedWide = 1;
+struct PagedPlan {
+    int kind;
+    int tile_rows;
+    int tiles;       // upper bound of the batch's query tiles
+    int splits;
+    int split_keys;
+    int64_t bytes;       // workspace of this call
+    int64_t most_bytes;  // of any window and shorter key axis at these sizes
+};
+// false: the batch has more tiles than a launch can name
+bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int64_t max_chunk,
+                int64_t max_kv_len, int64_t window, PagedPlan& plan);
+cudaError_t launch_paged_attention(const PagedParams& p, const PagedPlan& plan, int head_dim, cudaStream_t stream);
+
+cudaError_t launch_rope_cache(const RopeCacheParams& p, int head_dim, int rope_mode, cudaStream_t stream);
 cudaError_t launch_frames_to_u8(const FramesParams& p, cudaStream_t stream);
 cudaError_t launch_qk_rmsnorm_rope(const QkParams& p, int head_dim, int rope_mode, cudaStream_t stream);
 cudaError_t launch_adaln_modulate(const AdalnParams& p, cudaStream_t stream);
@@ -172,5 +244,8 @@ cudaError_t launch_validate_seqlens(const Packing& pk, int64_t num_rows_padded, 
 
 // Largest hidden size dit_adaln_modulate supports (8 warps x 8 vectors x 32 lanes x 8).
 constexpr int kMaxAdalnHidden = 16384;
+
+// Key heads of dit_paged_attention: a launch's second grid axis.
+constexpr int kMaxKvHeads = 65535;
 
 }  // namespace dit

@@ -19,6 +19,7 @@
 // 4 bytes per element.
 #include "common.cuh"
 #include "launch.h"
+#include "rope.cuh"
 
 namespace dit {
 namespace {
@@ -31,20 +32,6 @@ constexpr int kQkWarps = 4;
 // Steps per head batch (head vectors per lane in one batch): 4, or 2 when
 // 4-step batches would leave over a quarter of their head slots empty (see
 // launch_d).
-
-// angle mod 2*pi in fp64, then single precision: keeps the angle exact to
-// ~1e-7 rad for any position.  On the reduced angle, in [-pi, pi], the
-// hardware sine and cosine (__sincosf, absolute error ~1e-6 there) replace
-// the full-range sincosf: with 24 q + 4 k heads of 128 per row the per-row
-// setup is a large share of the work (long video 143.8 -> 141.3 us), and the
-// outputs move by at most one bf16 unit in ~1e-4 of the elements.
-__device__ __forceinline__ void pair_cos_sin(double angle, float& c, float& s)
-{
-    constexpr double kTwoPi = 6.283185307179586476925286766559;
-    constexpr double kInvTwoPi = 0.15915494309189533576888376337251;
-    const double red = angle - kTwoPi * rint(angle * kInvTwoPi);
-    __sincosf((float)red, &s, &c);
-}
 
 // b^k for 0 <= k < 128 (a pair index) by repeated squaring: the fp64 product
 // stays within ~1e-14 (relative) of theta^(-2j/d), far below what the fp32
@@ -259,51 +246,20 @@ qk_rmsnorm_rope_kernel(const __grid_constant__ QkParams p)  // read in place, ne
         sn[e] = 0.f;
     }
     if (MODE != kRopeNone) {
-        // Positions of this row: a row inside the sequence's T x H x W video
-        // grid (t-major, then h, then w) is 3D; every later row is 1D, counted
-        // from the end of the grid.  Without a grid every row is 1D.
         // g: the row's index in its whole sequence (the buffer may hold one
         // rank's slice of it, starting at row pos_offset[seq])
         // (a negative offset, outside the documented range, is read as 0, so
-        // every position stays >= 0 and the grid divisions below only run for
-        // a non-empty grid)
+        // every position stays >= 0 and the grid divisions only run for a
+        // non-empty grid)
         const int off = p.pos_offset != nullptr ? max(__ldg(p.pos_offset + s.seq), 0) : 0;
-        const long long g = (long long)s.local + off;
-        bool is3d = false;
-        long long pt = 0, ph = 0, pw = 0;
-        long long pos1 = g;
-        if (p.rope_grid != nullptr) {
-            const long long T = __ldg(p.rope_grid + 3 * s.seq);
-            const long long H = __ldg(p.rope_grid + 3 * s.seq + 1);
-            const long long W = __ldg(p.rope_grid + 3 * s.seq + 2);
-            const long long thw = T * H * W;
-            if (g < thw) {  // g >= 0, so the grid is non-empty here
-                is3d = true;
-                const long long hw = H * W;
-                if (hw > 0 && hw <= 0xffffffffLL) {
-                    // 32-bit divisions (g < 2^32 always): the row setup is a
-                    // large share of a narrow row's work (24 q + 4 k heads:
-                    // 146.4 -> 144.2 us, results unchanged)
-                    const unsigned gu = (unsigned)g, hwu = (unsigned)hw, wu = (unsigned)W;
-                    const unsigned t = gu / hwu, rem = gu - t * hwu, h = rem / wu;
-                    pt = t;
-                    ph = h;
-                    pw = rem - h * wu;
-                } else {
-                    pt = g / hw;
-                    ph = (g / W) % H;
-                    pw = g % W;
-                }
-            } else {
-                pos1 = g - thw;
-            }
-        }
+        const RowPosition rp = row_position((long long)s.local + off,
+                                            p.rope_grid != nullptr ? p.rope_grid + 3 * s.seq : nullptr);
         double f[NP];
         int ax[NP];
-        pair_frequencies<NP>(p, li, is3d, f, ax);
+        pair_frequencies<NP>(p, li, rp.is3d, f, ax);
 #pragma unroll
         for (int e = 0; e < NP; ++e) {
-            const long long pj = is3d ? (ax[e] == 0 ? pt : (ax[e] == 1 ? ph : pw)) : pos1;
+            const long long pj = rp.is3d ? (ax[e] == 0 ? rp.t : (ax[e] == 1 ? rp.h : rp.w)) : rp.line;
             pair_cos_sin((double)pj * f[e], cs[e], sn[e]);
         }
     }

@@ -1,0 +1,249 @@
+// rope_cache.cu -- rotary positions of q and k from a table of frequencies
+// (scaled for long contexts, over the first R elements of a head), optionally
+// behind the per-head RMSNorm, and the same on the way into a paged cache:
+// k rotated into its pages, v copied beside it.
+//
+//   y = x * rsqrt(mean(x^2) + eps) * w          (or x, without weights)
+//   (o_a, o_b) = g (y_a c - y_b s, y_a s + y_b c),  c, s = cos, sin(p f_j)
+// for the pairs j < R / 2: elements (2j, 2j + 1) interleaved, (j, j + R/2)
+// half-split; elements R .. D - 1 keep y.
+//
+// Bound: HBM, 4 bytes per element (read once, written once).  One warp per
+// row and run of heads: D / 8 lanes hold a head, 8 elements per lane, so a
+// lane needs the angles of the same 4 pairs for every head and forms them once
+// (the fp64 product p f_j, reduced, then the hardware sine and cosine).  The
+// heads go in batches of U steps, a batch's loads in flight while the one
+// before is computed.  A batch of few rows (next tokens) cannot fill the
+// GPU with whole rows: its rows' batches are spread over up to as many warps,
+// which repeats the angles and shortens the chain of loads (rows_per_run
+// below).  q, k and v are batched apart, so a batch has one weight vector and
+// one destination rule.
+#include "common.cuh"
+#include "launch.h"
+#include "rope.cuh"
+
+namespace dit {
+namespace {
+
+constexpr int kRcWarps = 4;  // warps per CTA
+
+// Offset of the lane's first or second quad of a head's elements.  A half-
+// split lane whose pairs turn holds 4 li .. and R/2 + 4 li ..; every other
+// lane holds 8 consecutive elements, which are its four interleaved pairs
+// (with R a multiple of 8 the lanes li < R / 8 turn and the rest pass).
+template <int MODE>
+__device__ __forceinline__ int quad_off(int li, int part, bool turns, int half)
+{
+    if (MODE == kRopeHalf && turns)
+        return part * half + 4 * li;
+    return 8 * li + 4 * part;
+}
+
+template <int MODE>
+__device__ __forceinline__ uint4 load_quads(const uint16_t* head, int o0, int o1)
+{
+    if (MODE == kRopeHalf) {
+        const uint2 a = __ldcs(reinterpret_cast<const uint2*>(head + o0));
+        const uint2 b = __ldcs(reinterpret_cast<const uint2*>(head + o1));
+        return make_uint4(a.x, a.y, b.x, b.y);
+    }
+    return ld_stream(head + o0);
+}
+
+// Cache pages are read again soon by the attention over them, so they keep
+// the default policy; rows of q and k go out evict-first like the other
+// operators' activations.
+template <int MODE>
+__device__ __forceinline__ void store_quads(uint16_t* head, int o0, int o1, uint4 v, bool keep)
+{
+    if (MODE == kRopeHalf) {
+        uint2* a = reinterpret_cast<uint2*>(head + o0);
+        uint2* b = reinterpret_cast<uint2*>(head + o1);
+        if (keep) {
+            *a = make_uint2(v.x, v.y);
+            *b = make_uint2(v.z, v.w);
+        } else {
+            __stcs(a, make_uint2(v.x, v.y));
+            __stcs(b, make_uint2(v.z, v.w));
+        }
+        return;
+    }
+    if (keep)
+        *reinterpret_cast<uint4*>(head + o0) = v;
+    else
+        st_stream(head + o0, v);
+}
+
+template <int D, int MODE, bool NORM, int U>
+__global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __grid_constant__ RopeCacheParams p)
+{
+    constexpr int LPH = D / 8;          // lanes per head
+    constexpr int HPW = kWarp / LPH;    // heads per step
+    constexpr int HB = HPW * U;         // heads per batch
+    grid_dependency_wait();
+    const int lane = threadIdx.x & (kWarp - 1);
+    const long long task = (long long)blockIdx.x * kRcWarps + (threadIdx.x >> 5);
+    const int v_row = (int)(task / p.runs_per_row);
+    const int run = (int)(task - (long long)v_row * p.runs_per_row);
+    RowSlot s;
+    if (!map_valid_row(v_row, p.pk.cu_seqlens, p.pk.cu_seqlens_padded, p.pk.num_seqs, p.pk.num_rows_padded, lane, s))
+        return;
+    const int sub = lane / LPH, li = lane % LPH;
+    const int nq = (p.num_q_heads + HB - 1) / HB, nk = (p.num_k_heads + HB - 1) / HB;
+    const int total = nq + nk + (p.v != nullptr ? nk : 0);
+    const int b0 = run * p.batches_per_run, b1 = min(b0 + p.batches_per_run, total);
+    if (b0 >= b1)
+        return;
+    const bool turns = li < (p.rotary_dim >> 3);
+    const int half = p.rotary_dim >> 1;
+    const int o0 = quad_off<MODE>(li, 0, turns, half), o1 = quad_off<MODE>(li, 1, turns, half);
+
+    // Where the row's k and v go: the rows' own outputs, or the token's slot
+    // in the cache.  A token whose slot the table does not name is dropped.
+    const int before = p.cache_lens != nullptr ? max(__ldg(p.cache_lens + s.seq), 0) : 0;
+    uint16_t* k_to = nullptr;
+    uint16_t* v_to = nullptr;
+    int64_t head_step = D;
+    if (p.block_table != nullptr) {
+        const long long slot = (long long)before + s.local;
+        const long long entry = slot / p.page_size;
+        if (entry < p.max_pages) {
+            const int page = __ldg(p.block_table + (int64_t)s.seq * p.table_stride + entry);
+            if (page >= 0 && page < p.num_pages) {
+                const int64_t at = (int64_t)page * p.page_stride + (slot - entry * p.page_size) * p.slot_stride;
+                k_to = p.k_cache + at;
+                v_to = p.v_cache + at;
+            }
+        }
+        head_step = p.head_stride;
+    } else if (p.k_out != nullptr) {
+        k_to = p.k_out + (int64_t)s.row * p.k_out_stride;
+    }
+    const uint16_t* q_from = p.q + (int64_t)s.row * p.q_row_stride;
+    const uint16_t* k_from = p.k + (int64_t)s.row * p.k_row_stride;
+    const uint16_t* v_from = p.v + (int64_t)s.row * p.v_row_stride;
+    uint16_t* q_to = p.q_out + (int64_t)s.row * p.q_out_stride;
+
+    auto load = [&](int b, uint4 (&x)[U]) {
+        const uint16_t* from = b < nq ? q_from : (b < nq + nk ? k_from : v_from);
+        const int heads = b < nq ? p.num_q_heads : p.num_k_heads;
+        const int h0 = (b < nq ? b : (b < nq + nk ? b - nq : b - nq - nk)) * HB + sub;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * HPW;
+            x[u] = h < heads ? load_quads<MODE>(from + (int64_t)h * D, o0, o1) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    uint4 cur[U];
+    load(b0, cur);
+
+    // cos and sin (times g) of the lane's four pairs
+    float c[4], sn[4];
+    if (turns && b0 < nq + nk) {
+        const int off = p.pos_offset != nullptr ? max(__ldg(p.pos_offset + s.seq), 0) : before;
+        const RowPosition rp = row_position((long long)s.local + off,
+                                            p.rope_grid != nullptr ? p.rope_grid + 3 * s.seq : nullptr);
+        const double2* table = reinterpret_cast<const double2*>(rp.is3d ? p.grid_freqs : p.freqs) + 2 * li;
+        const double2 f01 = __ldg(table), f23 = __ldg(table + 1);
+        const double f[4] = {f01.x, f01.y, f23.x, f23.y};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = 4 * li + e;
+            const long long at = !rp.is3d ? rp.line : (j < p.sec_pairs[0] ? rp.t
+                                                       : (j < p.sec_pairs[0] + p.sec_pairs[1] ? rp.h : rp.w));
+            pair_cos_sin((double)at * f[e], c[e], sn[e]);
+            c[e] *= p.attn_scale;
+            sn[e] *= p.attn_scale;
+        }
+    }
+
+    for (int b = b0; b < b1; ++b) {
+        uint4 nxt[U];
+        if (b + 1 < b1)
+            load(b + 1, nxt);
+        const bool is_q = b < nq, is_v = b >= nq + nk;
+        uint16_t* to = is_q ? q_to : (is_v ? v_to : k_to);
+        const int64_t step = is_q ? D : head_step;
+        const int heads = is_q ? p.num_q_heads : p.num_k_heads;
+        const int h0 = (is_q ? b : (is_v ? b - nq - nk : b - nq)) * HB + sub;
+        const bool keep = !is_q && p.block_table != nullptr;
+        float w[8];
+        if (NORM && !is_v) {
+            const uint16_t* wp = is_q ? p.q_weight : p.k_weight;
+            const uint2 wa = __ldg(reinterpret_cast<const uint2*>(wp + o0));
+            const uint2 wb = __ldg(reinterpret_cast<const uint2*>(wp + o1));
+            unpack8(make_uint4(wa.x, wa.y, wb.x, wb.y), w);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + u * HPW;
+            uint4 out = cur[u];
+            if (!is_v) {
+                float x[8], o[8];
+                unpack8(cur[u], x);
+                if (NORM) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        ss = fmaf(x[e], x[e], ss);
+                    ss = group_sum<LPH>(ss);  // every lane of the warp takes part
+                    const float r = rsqrtf(ss * (1.0f / (float)D) + p.eps);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] *= r * w[e];
+                }
+                if (turns) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int a = MODE == kRopeHalf ? e : 2 * e, z = MODE == kRopeHalf ? 4 + e : 2 * e + 1;
+                        o[a] = fmaf(x[a], c[e], -x[z] * sn[e]);
+                        o[z] = fmaf(x[a], sn[e], x[z] * c[e]);
+                    }
+                    out = pack8(o);
+                } else if (NORM) {
+                    out = pack8(x);
+                }  // else the element passes bit for bit
+            }
+            if (h < heads && to != nullptr)
+                store_quads<MODE>(to + (int64_t)h * step, o0, o1, out, keep);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            cur[u] = nxt[u];
+    }
+}
+
+template <int D, int U>
+cudaError_t launch_rc(RopeCacheParams p, int mode, cudaStream_t stream)
+{
+    constexpr int HB = (kWarp / (D / 8)) * U;
+    const int nk = (p.num_k_heads + HB - 1) / HB;
+    const int total = (p.num_q_heads + HB - 1) / HB + nk + (p.v != nullptr ? nk : 0);
+    // Runs per row: one warp takes a whole row once the rows alone give every
+    // SM 16 warps; below that a row's batches are spread over more warps.
+    const long long want = (148LL * 16 + p.pk.num_rows_padded - 1) / p.pk.num_rows_padded;
+    const int runs = (int)(want < total ? want : total);
+    p.batches_per_run = (total + runs - 1) / runs;
+    p.runs_per_row = (total + p.batches_per_run - 1) / p.batches_per_run;
+    const unsigned grid = (unsigned)(((long long)p.pk.num_rows_padded * p.runs_per_row + kRcWarps - 1) / kRcWarps);
+    const bool norm = p.k_weight != nullptr;
+    if (mode == kRopeHalf)
+        return norm ? launch_kernel(rope_cache_kernel<D, kRopeHalf, true, U>, grid, kRcWarps * kWarp, 0, stream, p)
+                    : launch_kernel(rope_cache_kernel<D, kRopeHalf, false, U>, grid, kRcWarps * kWarp, 0, stream, p);
+    return norm ? launch_kernel(rope_cache_kernel<D, kRopeInterleaved, true, U>, grid, kRcWarps * kWarp, 0, stream, p)
+                : launch_kernel(rope_cache_kernel<D, kRopeInterleaved, false, U>, grid, kRcWarps * kWarp, 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_cache(const RopeCacheParams& p, int head_dim, int rope_mode, cudaStream_t stream)
+{
+    switch (head_dim) {
+    case 64: return launch_rc<64, 2>(p, rope_mode, stream);
+    case 128: return launch_rc<128, 4>(p, rope_mode, stream);
+    case 256: return launch_rc<256, 4>(p, rope_mode, stream);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace dit
