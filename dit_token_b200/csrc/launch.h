@@ -202,6 +202,7 @@ struct PagedParams {
 // Which kernel a call takes, and how the key axis is cut.
 constexpr int kPagedNarrow = 0;
 constexpr int kPagedWide = 1;
+constexpr int kPagedTc = 2;
 struct PagedPlan {
     int kind;
     int tile_rows;
@@ -214,6 +215,7 @@ struct PagedPlan {
 // false: the batch has more tiles than a launch can name
 bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int64_t max_chunk,
                 int64_t max_kv_len, int64_t window, PagedPlan& plan);
+cudaError_t launch_paged_attention_tc(const PagedParams& p, int tiles, int head_dim, cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedParams& p, const PagedPlan& plan, int head_dim, cudaStream_t stream);
 
 cudaError_t launch_rope_cache(const RopeCacheParams& p, int head_dim, int rope_mode, cudaStream_t stream);

@@ -394,7 +394,8 @@ cudaError_t launch_shape(const PagedParams& p, int tiles, cudaStream_t stream)
 template <int D>
 cudaError_t launch_d(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream)
 {
-    const cudaError_t e = plan.kind == kPagedNarrow ? launch_shape<D, 1, 4, 64, D == 256 ? 2 : 3>(p, plan.tiles, stream)
+    const cudaError_t e = plan.kind == kPagedTc ? launch_paged_attention_tc(p, plan.tiles, D, stream)
+                          : plan.kind == kPagedNarrow ? launch_shape<D, 1, 4, 64, D == 256 ? 2 : 3>(p, plan.tiles, stream)
                                                     : launch_shape<D, 4, 1, 64, D == 256 ? 2 : 3>(p, plan.tiles, stream);
     if (e != cudaSuccess || p.splits == 1)
         return e;
@@ -410,8 +411,8 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
 {
     const int64_t group = num_q_heads / num_kv_heads;
     const int64_t chunk = max_chunk > 0 && max_chunk < rows ? max_chunk : rows;
-    plan.kind = chunk * group <= 32 ? kPagedNarrow : kPagedWide;
-    plan.tile_rows = plan.kind == kPagedNarrow ? 16 : 64;
+    plan.kind = chunk * group <= 32 ? kPagedNarrow : (head_dim == 256 ? kPagedWide : kPagedTc);
+    plan.tile_rows = plan.kind == kPagedNarrow ? 16 : (plan.kind == kPagedWide ? 64 : 256);
     // ceil over each sequence adds at most one tile per sequence
     const int64_t tiles = rows * group / plan.tile_rows + (num_seqs < rows ? num_seqs : rows);
     if (tiles > INT32_MAX)
@@ -436,9 +437,9 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
     // what one workspace must hold for every window and shorter length
     plan.most_bytes = splits == 1 ? 0 : part * splits;
     int64_t run = (keys + splits - 1) / splits;
-    run = (run + 63) / 64 * 64;
-    if (run < 64)
-        run = 64;
+    run = (run + 127) / 128 * 128;
+    if (run < 128)
+        run = 128;
     splits = (keys + run - 1) / run;
     plan.splits = (int)(splits < 1 ? 1 : splits);
     plan.split_keys = (int)(run > INT32_MAX ? INT32_MAX : run);

@@ -1,0 +1,565 @@
+// paged_attention_tc.cu -- attention of a chunk of new tokens over a paged
+// cache on the fifth-generation tensor cores (tcgen05, accumulators in tensor
+// memory), for heads of 64 and 128.
+//
+// The mathematics is paged_attention.cu's: one pass over the keys with the
+// running maximum m, sum l and unnormalised o of a softmax, in fp32, the
+// probabilities rounded to bf16 for their product with v.  The running
+// maximum may lag: o and l are rescaled only when a row's maximum has grown
+// by more than 2^8 since the last time, so probabilities reach at most 2^8
+// (bf16 has fp32's range: the relative rounding is unchanged) and almost every
+// tile skips the rescale.
+//
+// One block takes 256 rows, two tiles of 128 (a row is a (token, head) pair of
+// one key head's group), over 128 keys at a time:
+//   warps 0-3, 4-7  softmax of tile 0 and of tile 1; a thread owns a row, so
+//                   row maxima and sums need no exchange
+//   warp 8          issues the products: s = q k^T (both from shared memory)
+//                   and o += p v (p from tensor memory)
+//   warps 9-11      copy q, k and v to shared memory with 16-byte asynchronous
+//                   copies: any page size and stride, and zeros for keys that
+//                   are not there (0 * NaN must not reach the sums)
+// The two tiles alternate: while one's softmax runs, the other's products do.
+// Tensor memory (512 columns of 128 lanes x 32 bits): s0, s1 (128 each), o0,
+// o1 (D each); p takes the first half of its s, once the row is in registers.
+// The products of one tile are issued in the order o(i), s(i+1), and a
+// commit covers everything issued before it, so "s(i+1) is there" also says
+// that o(i) is complete and p(i) is free.
+//
+// Every wait is bounded: a wait that gives up raises a flag that ends the
+// block's other waits, and the block's rows become NaN.
+#include "paged.cuh"
+
+namespace dit {
+namespace {
+
+constexpr int kTcRows = 128;   // rows per tile
+constexpr int kTcKeys = 128;   // keys per step
+constexpr int kTcThreads = 384;
+constexpr int kTcCopyThreads = 96;
+constexpr uint32_t kBlockBytes = kTcKeys * 128;  // 128 rows of 64 elements
+constexpr float kTcLag = 8.f;  // log2 of how far probabilities may pass 1
+constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after two seconds
+
+template <int D>
+struct TcShape {
+    static constexpr int kSlots = D == 128 ? 4 : 8;              // key or value tiles in shared memory
+    static constexpr uint32_t kTile = (D / 64) * kBlockBytes;    // bytes of a tile (q, k or v)
+    static constexpr uint32_t kQ = 0;                            // two query tiles
+    static constexpr uint32_t kRing = 2 * kTile;
+    static constexpr uint32_t kBars = kRing + kSlots * kTile;
+    static constexpr int kNumBars = 2 * kSlots + 8;
+    static constexpr uint32_t kTmemPtr = kBars + kNumBars * 8;
+    static constexpr uint32_t kAbort = kTmemPtr + 4;
+    static constexpr uint32_t kSmem = kAbort + 4;
+};
+
+// ------------------------------------------------------------- barriers
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns()
+{
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort)
+{
+    const unsigned long long from = now_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try(bar, parity))
+                return true;
+        if (*abort != 0)
+            return false;
+        if (now_ns() - from > kWaitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort)
+{
+    return mbar_try(bar, parity) || mbar_wait_long(bar, parity, abort);
+}
+
+// ------------------------------------------------------------- tcgen05
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// d (+)= a b^T, a and b in shared memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "r"((uint32_t)add) : "memory");
+}
+// d (+)= a b, a in tensor memory, b in shared memory
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+                 "r"((uint32_t)add) : "memory");
+}
+
+// 32 columns of the thread's lane.
+__device__ __forceinline__ void tc_ld32(uint32_t addr, float* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                   "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]),
+                   "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]),
+                   "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]),
+                   "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+                 "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+                 "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+                 "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+                 "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+}
+// The loads before have landed.  The registers pass through, so that nothing
+// that reads them moves above the wait.
+__device__ __forceinline__ void tc_tie32(float* r)
+{
+    asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]),
+                       "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]),
+                       "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]),
+                       "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]),
+                       "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                       "+f"(r[30]), "+f"(r[31]));
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory matrix descriptor, rows of 128 bytes permuted in 16-byte chunks
+// by the row's low 3 bits (128-byte swizzle), 8-row groups 1024 bytes apart.
+// `lead` (16-byte units) is the distance of 64-element blocks along the
+// contiguous axis, read only where that axis is the product's outer one (v).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead)
+{
+    return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)lead << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: bf16 operands, fp32 accumulator, M x N, b along its
+// inner axis (s = q k^T) or its outer one (o = p v).
+template <int M, int N, bool B_OUTER>
+struct TcIdesc {
+    static constexpr uint32_t value = (1u << 4) | (1u << 7) | (1u << 10) | ((B_OUTER ? 1u : 0u) << 16) |
+                                      ((uint32_t)(N / 8) << 17) | ((uint32_t)(M / 16) << 24);
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile of 128 rows.
+__device__ __forceinline__ uint32_t tc_off(int r, int c)
+{
+    return (uint32_t)(c >> 3) * kBlockBytes + (uint32_t)(r * 128 + (((c ^ r) & 7) << 4));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const __grid_constant__ PagedParams p)
+{
+    using S = TcShape<D>;
+    constexpr int NS = S::kSlots;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    grid_dependency_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int kvh = blockIdx.y, split = blockIdx.z;
+    QueryTile q;
+    // later tiles of a causal chunk see more keys: they go first
+    if (!map_query_tile((int)(gridDim.x - 1 - blockIdx.x), p, 2 * kTcRows, lane, q))
+        return;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kAbort);
+    const uint32_t bars = base + S::kBars;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (NS + s); };
+    const uint32_t q_full = bars + 8u * (2 * NS);
+    auto s_full = [&](int t) { return bars + 8u * (2 * NS + 1 + t); };
+    auto p_full = [&](int t) { return bars + 8u * (2 * NS + 3 + t); };
+    auto o_full = [&](int t) { return bars + 8u * (2 * NS + 5 + t); };
+    const uint32_t drained = bars + 8u * (2 * NS + 7);
+
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full(s), kTcCopyThreads);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(q_full, kTcCopyThreads);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full(t), 1);
+            mbar_init(p_full(t), kTcRows);
+            mbar_init(o_full(t), 1);
+        }
+        mbar_init(drained, 1);
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + S::kTmemPtr) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kTmemPtr);
+
+    // Keys of the two tiles, the block's share of them, and each tile's steps
+    // [first, last) of the block's.
+    int lo[2], hi[2], rows[2], unused;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        rows[t] = min(max(q.rows - t * kTcRows, 0), kTcRows);
+        lo[t] = 0;
+        hi[t] = 0;
+        if (rows[t] > 0) {
+            visible_keys(p, q, (q.first + t * kTcRows) / p.group, lo[t], unused);
+            visible_keys(p, q, (q.first + t * kTcRows + rows[t] - 1) / p.group, unused, hi[t]);
+        }
+    }
+    int k_lo = lo[0], k_hi = max(hi[0], hi[1]);
+    if (p.splits > 1) {
+        const long long from = k_lo + (long long)split * p.split_keys;
+        if (split + 1 < p.splits)
+            k_hi = (int)min((long long)k_hi, from + p.split_keys);
+        k_lo = (int)min(from, (long long)max(k_hi, 0));
+    }
+    int first[2], last[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int top = min(hi[t], k_hi);
+        first[t] = max(lo[t] - k_lo, 0) / kTcKeys;
+        last[t] = top > k_lo ? (top - k_lo + kTcKeys - 1) / kTcKeys : 0;
+        if (rows[t] == 0 || last[t] <= first[t])
+            first[t] = last[t] = 0;
+    }
+    const int steps = max(last[0], last[1]);
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {
+            if (lane == 0) {
+                constexpr uint32_t kIdescS = TcIdesc<kTcRows, kTcKeys, false>::value;
+                constexpr uint32_t kIdescO = TcIdesc<kTcRows, D, true>::value;
+                auto in = [&](int t, int i) { return i >= first[t] && i < last[t]; };
+                auto scores = [&](int t, int slot) {
+                    const uint32_t a = base + S::kQ + t * S::kTile, b = base + S::kRing + slot * S::kTile;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = (uint32_t)(ks >> 2) * kBlockBytes + (uint32_t)(ks & 3) * 32;
+                        tc_mma_ss(tmem + t * kTcKeys, smem_desc(a + off, 1), smem_desc(b + off, 1), kIdescS, ks > 0);
+                    }
+                    tc_commit(s_full(t));
+                };
+                auto products = [&](int t, int slot, bool add) {
+                    const uint32_t b = base + S::kRing + slot * S::kTile;
+#pragma unroll
+                    for (int ks = 0; ks < kTcKeys / 16; ++ks)
+                        tc_mma_ts(tmem + 2 * kTcKeys + t * D, tmem + t * kTcKeys + ks * 8,
+                                  smem_desc(b + ks * 2048, kBlockBytes >> 4), kIdescO, add || ks > 0);
+                };
+                bool go = steps > 0 && mbar_wait(q_full, 0, abort) && mbar_wait(full(0), 0, abort);
+                if (go) {
+                    tc_fence_after();
+                    for (int t = 0; t < 2; ++t)
+                        if (in(t, 0))
+                            scores(t, 0);
+                    tc_commit(empty(0));
+                }
+                for (int i = 0; go && i < steps; ++i) {
+                    const int vt = 2 * i + 1, kt = 2 * i + 2;
+                    const int vs = vt % NS, ks = kt % NS;
+                    go = mbar_wait(full(vs), (uint32_t)(vt / NS) & 1u, abort);
+                    if (go && i + 1 < steps)
+                        go = mbar_wait(full(ks), (uint32_t)(kt / NS) & 1u, abort);
+                    for (int t = 0; go && t < 2; ++t) {
+                        if (in(t, i)) {
+                            go = mbar_wait(p_full(t), (uint32_t)(i - first[t]) & 1u, abort);
+                            if (!go)
+                                break;
+                            tc_fence_after();
+                            products(t, vs, i > first[t]);
+                            if (i + 1 == last[t])
+                                tc_commit(o_full(t));
+                        }
+                        if (t == 1)
+                            tc_commit(empty(vs));
+                        if (in(t, i + 1))
+                            scores(t, ks);
+                    }
+                    if (go && i + 1 < steps)
+                        tc_commit(empty(ks));
+                }
+                if (!go && steps > 0) {  // given up: let what was issued end before the memory is freed
+                    tc_commit(drained);
+                    const unsigned long long from = now_ns();
+                    while (!mbar_try(drained, 0) && now_ns() - from < kWaitNs) {
+                    }
+                }
+            }
+            __syncwarp();
+        } else {
+            // Groups of copies in order: q, then k and v of each step.  A
+            // group is reported (after it has landed and a fence has handed it
+            // to the tensor cores) two groups later, or at once when there is
+            // no room to copy further.
+            const int cw = warp - 9;
+            const int ct = tid - 9 * 32;
+            constexpr int CH = D / 8;          // chunks per row
+            constexpr int RPI = 32 / CH;       // rows per warp instruction
+            const int32_t* table = p.block_table + (int64_t)q.seq * p.table_stride;
+            const uint16_t* kc = p.k_cache + (int64_t)kvh * p.head_stride;
+            const uint16_t* vc = p.v_cache + (int64_t)kvh * p.head_stride;
+            if (steps > 0) {
+                for (int e = ct; e < 2 * kTcRows * CH; e += kTcCopyThreads) {
+                    const int r = e / CH, c = e % CH;
+                    const bool there = r < q.rows;
+                    const int at = q.first + (there ? r : 0), token = at / p.group, head = kvh * p.group + at % p.group;
+                    cp_async16(base + S::kQ + (r >= kTcRows ? S::kTile : 0) + tc_off(r & (kTcRows - 1), c),
+                               p.q + (int64_t)(q.row0 + token) * p.q_row_stride + head * D + c * 8, there);
+                }
+                cp_async_commit();
+            }
+            int told = 0;  // groups reported
+            auto tell = [&](int group) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(group == 0 ? q_full : full((group - 1) % NS));
+            };
+            int64_t offs[4], next[4];
+            auto look_up = [&](int i, int64_t (&o)[4]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = k_lo + i * kTcKeys + e * 32 + lane;
+                    o[e] = key < k_hi ? key_offset(p, table, key) : -1;
+                }
+            };
+            if (steps > 0)
+                look_up(0, next);
+            bool go = true;
+            for (int j = 0; go && j < 2 * steps; ++j) {
+                const int slot = j % NS;
+                if ((j & 1) == 0) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        offs[e] = next[e];
+                    if (j / 2 + 1 < steps)
+                        look_up(j / 2 + 1, next);
+                }
+                if (j >= NS) {
+                    const uint32_t parity = (uint32_t)(j / NS - 1) & 1u;
+                    if (!__all_sync(0xffffffffu, mbar_try(empty(slot), parity))) {
+                        cp_async_wait<0>();
+                        while (told < j + 1)
+                            tell(told++);
+                        go = mbar_wait(empty(slot), parity, abort);
+                        go = __all_sync(0xffffffffu, go);
+                        if (!go)
+                            break;
+                    }
+                }
+                const uint16_t* from = (j & 1) ? vc : kc;
+                const uint32_t to = base + S::kRing + slot * S::kTile;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    for (int it = cw; it < 32 / RPI; it += 3) {
+                        const int rr = it * RPI + lane / CH, c = lane % CH;
+                        const int64_t o = __shfl_sync(0xffffffffu, offs[e], rr);
+                        cp_async16(to + tc_off(e * 32 + rr, c), from + (o >= 0 ? o : 0) + c * 8, o >= 0);
+                    }
+                cp_async_commit();
+                if (j + 2 - told > 2) {
+                    cp_async_wait<2>();
+                    tell(told++);
+                }
+            }
+            cp_async_wait<0>();
+            if (go && steps > 0)
+                while (told < 2 * steps + 1)
+                    tell(told++);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int t = warp >> 2;
+        const int r = tid & (kTcRows - 1);
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes: bits 16 and up, times 32
+        const uint32_t s_at = tmem + t * kTcKeys + lanes, o_at = tmem + 2 * kTcKeys + t * D + lanes;
+        const bool mine = r < rows[t];
+        const int at = q.first + t * kTcRows + min(r, max(rows[t] - 1, 0));
+        const int token = at / p.group, head = kvh * p.group + at % p.group;
+        int r_lo, r_hi;
+        visible_keys(p, q, token, r_lo, r_hi);
+        r_hi = min(r_hi, k_hi);
+        float m = -INFINITY, l = 0.f;
+        bool go = true;
+        const int n0 = first[t], n1 = last[t];
+        for (int i = n0; i < n1; ++i) {
+            go = mbar_wait(s_full(t), (uint32_t)(i - n0) & 1u, abort);
+            go = __all_sync(0xffffffffu, go);
+            if (!go)
+                break;
+            tc_fence_after();
+            float s[kTcKeys];
+#pragma unroll
+            for (int c = 0; c < kTcKeys; c += 32)
+                tc_ld32(s_at + c, s + c);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kTcKeys; c += 32)
+                tc_tie32(s + c);
+            const int k0 = k_lo + i * kTcKeys;
+            if (!__all_sync(0xffffffffu, r_lo <= k0 && r_hi >= k0 + kTcKeys)) {
+#pragma unroll
+                for (int c = 0; c < kTcKeys; ++c)
+                    if (k0 + c < r_lo || k0 + c >= r_hi)
+                        s[c] = -INFINITY;
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < kTcKeys; ++c)
+                top[c & 3] = fmaxf(top[c & 3], s[c]);
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
+            if (i == n0) {
+                m = mx;
+            } else if (__any_sync(0xffffffffu, mx > m + kTcLag)) {
+                const float mn = mx > m + kTcLag ? mx : m;
+                const float f = m == mn ? 1.f : ex2(m - mn);  // -inf stays -inf until a key is seen
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tc_ld32(o_at + c, o);
+                    tc_wait_ld();
+                    tc_tie32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] *= f;
+                    tc_st32(o_at + c, reinterpret_cast<const uint32_t*>(o));
+                }
+            }
+            const float base_m = m == -INFINITY ? 0.f : m;
+            const f32x2 scale2 = f2_make(p.scale_log2, p.scale_log2), base2 = f2_make(-base_m, -base_m);
+            f32x2 sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    f32x2 e = f2_fma(f2_make(s[64 * h + 2 * c], s[64 * h + 2 * c + 1]), scale2, base2);
+                    e.x = ex2(e.x);
+                    e.y = ex2(e.y);
+                    sum[c & 1] = f2_add(sum[c & 1], e);
+                    pk[c] = f2_to_bf16x2(e);
+                }
+                tc_st32(s_at + 32 * h, pk);
+            }
+            sum[0] = f2_add(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(p_full(t));
+        }
+        if (go && n1 > n0) {
+            go = mbar_wait(o_full(t), 0, abort);
+            go = __all_sync(0xffffffffu, go);
+            tc_fence_after();
+        }
+        // the thread's row: output, or the split's part
+        const bool whole = p.splits == 1;
+        const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
+        const int64_t part = partial_index(p, q.ordinal0 + token, head, split);
+        uint16_t* out = p.out + (int64_t)(q.row0 + token) * p.out_row_stride + head * D;
+        float* part_o = whole ? nullptr : p.part_o + part * D;
+        if (n1 > n0 || whole) {
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    o[e] = 0.f;
+                if (n1 > n0) {  // uniform over the warpgroup
+                    tc_ld32(o_at + c, o);
+                    tc_wait_ld();
+                    tc_tie32(o);
+                }
+                if (!go)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = NAN;
+                if (!mine)
+                    continue;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(out + c + e) =
+                            make_uint4(pack2(o[e] * inv, o[e + 1] * inv), pack2(o[e + 2] * inv, o[e + 3] * inv),
+                                       pack2(o[e + 4] * inv, o[e + 5] * inv), pack2(o[e + 6] * inv, o[e + 7] * inv));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(part_o + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+        }
+        if (mine) {
+            if (!whole)
+                p.part_ml[part] = make_float2(n1 > n0 ? (go ? m : NAN) : -INFINITY, l);
+            else if (p.lse != nullptr)
+                p.lse[(int64_t)(q.row0 + token) * p.num_q_heads + head] = (m + log2f(l)) * kLn2;
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D>
+cudaError_t launch_tc(const PagedParams& p, int tiles, cudaStream_t stream)
+{
+    auto* kernel = paged_attention_tc_kernel<D>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    return launch_kernel(kernel, dim3((unsigned)tiles, (unsigned)p.num_kv_heads, (unsigned)p.splits), kTcThreads,
+                         TcShape<D>::kSmem, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attention_tc(const PagedParams& p, int tiles, int head_dim, cudaStream_t stream)
+{
+    return head_dim == 128 ? launch_tc<128>(p, tiles, stream) : launch_tc<64>(p, tiles, stream);
+}
+
+}  // namespace dit
