@@ -76,11 +76,17 @@ __device__ __forceinline__ void visible_keys(const PagedParams& p, const QueryTi
     lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 
+// The entry of a sequence's table that holds a token.
+__device__ __forceinline__ unsigned page_of(const PagedParams& p, int key)
+{
+    return (unsigned)(((unsigned long long)(unsigned)key * p.page_mul) >> p.page_shift);
+}
+
 // Element offset of a token's slot in the cache, or -1 where the table names
 // no page of the cache.
 __device__ __forceinline__ int64_t key_offset(const PagedParams& p, const int32_t* table, int key)
 {
-    const unsigned entry = (unsigned)(((unsigned long long)(unsigned)key * p.page_mul) >> p.page_shift);
+    const unsigned entry = page_of(p, key);
     const int page = __ldg(table + entry);
     if (page < 0 || page >= p.num_pages)
         return -1;
@@ -93,6 +99,10 @@ __device__ __forceinline__ int64_t key_offset(const PagedParams& p, const int32_
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

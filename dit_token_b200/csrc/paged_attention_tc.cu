@@ -39,7 +39,7 @@ constexpr int kTcThreads = 384;
 constexpr int kTcCopyThreads = 96;
 constexpr uint32_t kBlockBytes = kTcKeys * 128;  // 128 rows of 64 elements
 constexpr float kTcLag = 8.f;  // log2 of how far probabilities may pass 1
-constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after two seconds
+constexpr long long kWaitCycles = 4000000000ll;  // a wait gives up after about two seconds
 
 template <int D>
 struct TcShape {
@@ -70,22 +70,16 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
                  : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ unsigned long long now_ns()
-{
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
 __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, volatile int* abort)
 {
-    const unsigned long long from = now_ns();
+    const long long from = clock64();
     for (;;) {
         for (int i = 0; i < 64; ++i)
             if (mbar_try(bar, parity))
                 return true;
         if (*abort != 0)
             return false;
-        if (now_ns() - from > kWaitNs) {
+        if (clock64() - from > kWaitCycles) {
             *abort = 1;
             return false;
         }
@@ -95,6 +89,14 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 {
     return mbar_try(bar, parity) || mbar_wait_long(bar, parity, abort);
 }
+
+// The barrier counts this thread once its copies so far have landed.
+__device__ __forceinline__ void cp_async_report(uint32_t bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// Copies seen through a barrier become visible to the tensor cores' proxy.
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         mbar_init(drained, 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        proxy_fence();
     }
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + S::kTmemPtr) : "memory");
@@ -290,6 +292,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 };
                 bool go = steps > 0 && mbar_wait(q_full, 0, abort) && mbar_wait(full(0), 0, abort);
                 if (go) {
+                    proxy_fence();
                     tc_fence_after();
                     for (int t = 0; t < 2; ++t)
                         if (in(t, 0))
@@ -302,6 +305,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                     go = mbar_wait(full(vs), (uint32_t)(vt / NS) & 1u, abort);
                     if (go && i + 1 < steps)
                         go = mbar_wait(full(ks), (uint32_t)(kt / NS) & 1u, abort);
+                    proxy_fence();
                     for (int t = 0; go && t < 2; ++t) {
                         if (in(t, i)) {
                             go = mbar_wait(p_full(t), (uint32_t)(i - first[t]) & 1u, abort);
@@ -322,17 +326,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 }
                 if (!go && steps > 0) {  // given up: let what was issued end before the memory is freed
                     tc_commit(drained);
-                    const unsigned long long from = now_ns();
-                    while (!mbar_try(drained, 0) && now_ns() - from < kWaitNs) {
+                    const long long from = clock64();
+                    while (!mbar_try(drained, 0) && clock64() - from < kWaitCycles) {
                     }
                 }
             }
             __syncwarp();
         } else {
-            // Groups of copies in order: q, then k and v of each step.  A
-            // group is reported (after it has landed and a fence has handed it
-            // to the tensor cores) two groups later, or at once when there is
-            // no room to copy further.
+            // Each thread's copies into a slot report to the slot's barrier
+            // when they land (the issuing thread hands them to the tensor
+            // cores with a proxy fence), so copies for every free slot are
+            // under way at once.
             const int cw = warp - 9;
             const int ct = tid - 9 * 32;
             constexpr int CH = D / 8;          // chunks per row
@@ -348,64 +352,76 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                     cp_async16(base + S::kQ + (r >= kTcRows ? S::kTile : 0) + tc_off(r & (kTcRows - 1), c),
                                p.q + (int64_t)(q.row0 + token) * p.q_row_stride + head * D + c * 8, there);
                 }
-                cp_async_commit();
+                cp_async_report(q_full);
             }
-            int told = 0;  // groups reported
-            auto tell = [&](int group) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(group == 0 ? q_full : full((group - 1) % NS));
-            };
-            int64_t offs[4], next[4];
-            auto look_up = [&](int i, int64_t (&o)[4]) {
+            // A warp copies 44 of a tile's rows (the last one 40), RPI rows per
+            // instruction, CH lanes to a row.  Lane e holds where rows e and
+            // 32 + e of them lie; the page numbers are read a step ahead.
+            // Copying bounded the kernel while each row's place was looked up
+            // and permuted per copy: all that is left per copy is a shuffle
+            // of the offset and one addition (video chunk COPYFIG).
+            constexpr int kOwn = 44;
+            constexpr int kPatterns = 8 / RPI;  // rows of one instruction, modulo 8
+            const int r0 = cw * kOwn, own = min(kOwn, kTcKeys - r0), sub = lane / CH, c = lane % CH;
+            uint32_t dst[kPatterns];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = k_lo + i * kTcKeys + e * 32 + lane;
-                    o[e] = key < k_hi ? key_offset(p, table, key) : -1;
+            for (int e = 0; e < kPatterns; ++e)
+                dst[e] = base + S::kRing + tc_off(r0 + sub + e * RPI, c) - (uint32_t)(e * RPI * 128);
+            int page[2], slot_in[2];
+            auto look_up = [&](int i) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int key = k_lo + i * kTcKeys + r0 + 32 * e + lane;
+                    page[e] = -1;
+                    if (key < k_hi && 32 * e + lane < own) {
+                        const unsigned entry = page_of(p, key);
+                        slot_in[e] = key - (int)entry * p.page_size;
+                        page[e] = __ldg(table + entry);
+                    }
                 }
             };
+            int64_t offs[2];
+            uint32_t there[2];  // bit e: row 32 w + e can be read
+            bool all_there = false;
             if (steps > 0)
-                look_up(0, next);
+                look_up(0);
             bool go = true;
             for (int j = 0; go && j < 2 * steps; ++j) {
                 const int slot = j % NS;
                 if ((j & 1) == 0) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        offs[e] = next[e];
+                    for (int e = 0; e < 2; ++e) {
+                        const bool ok = page[e] >= 0 && page[e] < p.num_pages;
+                        offs[e] = ok ? (int64_t)page[e] * p.page_stride + (int64_t)slot_in[e] * p.slot_stride : 0;
+                        there[e] = __ballot_sync(0xffffffffu, ok);
+                    }
+                    all_there = there[0] == 0xffffffffu && (there[1] | (own == kOwn ? 0u : 0xf00u)) == 0xfffu;
                     if (j / 2 + 1 < steps)
-                        look_up(j / 2 + 1, next);
+                        look_up(j / 2 + 1);
                 }
                 if (j >= NS) {
                     const uint32_t parity = (uint32_t)(j / NS - 1) & 1u;
-                    if (!__all_sync(0xffffffffu, mbar_try(empty(slot), parity))) {
-                        cp_async_wait<0>();
-                        while (told < j + 1)
-                            tell(told++);
-                        go = mbar_wait(empty(slot), parity, abort);
-                        go = __all_sync(0xffffffffu, go);
-                        if (!go)
-                            break;
-                    }
+                    go = __all_sync(0xffffffffu, mbar_wait(empty(slot), parity, abort));
+                    if (!go)
+                        break;
                 }
-                const uint16_t* from = (j & 1) ? vc : kc;
-                const uint32_t to = base + S::kRing + slot * S::kTile;
+                const uint16_t* from = ((j & 1) ? vc : kc) + c * 8;
+                const uint32_t to = slot * S::kTile;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    for (int it = cw; it < 32 / RPI; it += 3) {
-                        const int rr = it * RPI + lane / CH, c = lane % CH;
-                        const int64_t o = __shfl_sync(0xffffffffu, offs[e], rr);
-                        cp_async16(to + tc_off(e * 32 + rr, c), from + (o >= 0 ? o : 0) + c * 8, o >= 0);
+                for (int it = 0; it < kOwn / RPI; ++it) {
+                    const int row = it * RPI;  // of the warp's, plus sub
+                    const int64_t o = __shfl_sync(0xffffffffu, offs[row / 32], (row % 32) + sub);
+                    const uint32_t at = to + dst[it % kPatterns] + (uint32_t)(row * 128);
+                    if (all_there) {
+                        if (row < own)
+                            cp_async16(at, from + o);
+                    } else if (row < own) {
+                        cp_async16(at, from + o, (there[row / 32] >> ((row % 32) + sub)) & 1u);
                     }
-                cp_async_commit();
-                if (j + 2 - told > 2) {
-                    cp_async_wait<2>();
-                    tell(told++);
                 }
+                cp_async_report(full(slot));
             }
-            cp_async_wait<0>();
-            if (go && steps > 0)
-                while (told < 2 * steps + 1)
-                    tell(told++);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
