@@ -610,9 +610,13 @@ dit_status dit_paged_attention_workspace(int64_t num_rows_padded, int32_t num_se
     if (num_seqs == 0 || num_rows_padded == 0)
         return DIT_OK;
     dit::PagedPlan plan{};
-    if (!dit::paged_plan(num_rows_padded, num_seqs, num_q_heads, num_kv_heads, head_dim, max_chunk, max_kv_len, 0, plan))
-        return DIT_ERR_SHAPE;
-    *bytes = plan.most_bytes;
+    // whatever the cache's strides let it take
+    for (const bool regular : {false, true}) {
+        if (!dit::paged_plan(num_rows_padded, num_seqs, num_q_heads, num_kv_heads, head_dim, max_chunk, max_kv_len, 0,
+                             regular, plan))
+            return DIT_ERR_SHAPE;
+        *bytes = plan.most_bytes > *bytes ? plan.most_bytes : *bytes;
+    }
     return DIT_OK;
 }
 
@@ -650,7 +654,11 @@ dit_status dit_paged_attention(const void* q, int64_t q_row_stride, const void* 
     int64_t keys = max_kv_len > 0 && max_kv_len < capacity ? max_kv_len : capacity;
     keys = keys < 1 ? 1 : (keys > INT32_MAX ? INT32_MAX : keys);
     dit::PagedPlan plan{};
-    if (!dit::paged_plan(num_rows_padded, num_seqs, num_q_heads, num_kv_heads, head_dim, max_chunk, keys, window, plan))
+    dit::CacheRows as_rows;
+    const bool regular = dit::cache_rows(page_stride, slot_stride, head_stride, num_pages, page_size, num_kv_heads,
+                                         head_dim, as_rows);
+    if (!dit::paged_plan(num_rows_padded, num_seqs, num_q_heads, num_kv_heads, head_dim, max_chunk, keys, window,
+                         regular, plan))
         return DIT_ERR_SHAPE;
     if (plan.bytes > workspace_bytes)
         return DIT_ERR_SHAPE;

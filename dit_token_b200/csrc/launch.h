@@ -197,7 +197,19 @@ struct PagedParams {
     float scale_log2;               // softmax scale times log2(e)
     int32_t causal, window;         // window 0: none
     int32_t splits, split_keys;
+    int32_t page_rows, head_rows, head_cols, box_rows;  // see CacheRows; set by the launcher that uses them
 };
+
+// A cache whose strides make it a matrix of rows slot_stride apart: slot s of
+// page g, head h is row g * page_rows + s + h * head_rows, columns from
+// h * head_cols.  box_rows: the largest power of two, at most 128, that divides
+// the page size.  false: its strides do not, or the page size is no multiple of 8.
+struct CacheRows {
+    int32_t page_rows, head_rows, head_cols, box_rows;
+    int64_t rows, cols;
+};
+bool cache_rows(int64_t page_stride, int64_t slot_stride, int64_t head_stride, int num_pages, int page_size,
+                int num_kv_heads, int head_dim, CacheRows& c);
 
 // Which kernel a call takes, and how the key axis is cut.
 constexpr int kPagedNarrow = 0;
@@ -213,8 +225,9 @@ struct PagedPlan {
     int64_t most_bytes;  // of any window and shorter key axis at these sizes
 };
 // false: the batch has more tiles than a launch can name
+// regular: cache_rows holds for the cache
 bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int64_t max_chunk,
-                int64_t max_kv_len, int64_t window, PagedPlan& plan);
+                int64_t max_kv_len, int64_t window, bool regular, PagedPlan& plan);
 cudaError_t launch_paged_attention_tc(const PagedParams& p, int tiles, int head_dim, cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedParams& p, const PagedPlan& plan, int head_dim, cudaStream_t stream);
 

@@ -407,11 +407,11 @@ cudaError_t launch_d(const PagedParams& p, const PagedPlan& plan, cudaStream_t s
 
 // The kernel, and the cut of the key axis, for a call's sizes.
 bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int64_t max_chunk,
-                int64_t max_kv_len, int64_t window, PagedPlan& plan)
+                int64_t max_kv_len, int64_t window, bool regular, PagedPlan& plan)
 {
     const int64_t group = num_q_heads / num_kv_heads;
     const int64_t chunk = max_chunk > 0 && max_chunk < rows ? max_chunk : rows;
-    plan.kind = chunk * group <= 32 ? kPagedNarrow : (head_dim == 256 ? kPagedWide : kPagedTc);
+    plan.kind = chunk * group <= 32 ? kPagedNarrow : (head_dim == 256 || !regular ? kPagedWide : kPagedTc);
     plan.tile_rows = plan.kind == kPagedNarrow ? 16 : (plan.kind == kPagedWide ? 64 : 256);
     // ceil over each sequence adds at most one tile per sequence
     const int64_t tiles = rows * group / plan.tile_rows + (num_seqs < rows ? num_seqs : rows);

@@ -16,9 +16,16 @@
 //                   row maxima and sums need no exchange
 //   warp 8          issues the products: s = q k^T (both from shared memory)
 //                   and o += p v (p from tensor memory)
-//   warps 9-11      copy q, k and v to shared memory with 16-byte asynchronous
-//                   copies: any page size and stride, and zeros for keys that
-//                   are not there (0 * NaN must not reach the sums)
+//   warp 9          fetches k and v with TMA, in boxes of rows that never cross
+//                   a page: the largest power of two that divides the page
+//                   size, 8 to 128 rows; and writes zeros over the last step's
+//                   rows of v behind the block's keys: the cache may hold
+//                   anything behind the last token, and 0 * NaN must not reach
+//                   the sums
+// The softmax warps first copy q.  (Fetching k and v with 16-byte asynchronous
+// copies by three warps held the video chunk at 3584 us, 2.8 us a step, and
+// gathering TMA copies of four rows at 6210; without any copies it took 2611.)
+// Steps begin at multiples of 128 keys, so boxes keep their alignment.
 // The two tiles alternate: while one's softmax runs, the other's products do.
 // Tensor memory (512 columns of 128 lanes x 32 bits): s0, s1 (128 each), o0,
 // o1 (D each); p takes the first half of its s, once the row is in registers.
@@ -28,6 +35,8 @@
 //
 // Every wait is bounded: a wait that gives up raises a flag that ends the
 // block's other waits, and the block's rows become NaN.
+#include <cuda.h>
+
 #include "paged.cuh"
 
 namespace dit {
@@ -36,7 +45,7 @@ namespace {
 constexpr int kTcRows = 128;   // rows per tile
 constexpr int kTcKeys = 128;   // keys per step
 constexpr int kTcThreads = 384;
-constexpr int kTcCopyThreads = 96;
+constexpr int kTcSoftmaxThreads = 256;
 constexpr uint32_t kBlockBytes = kTcKeys * 128;  // 128 rows of 64 elements
 constexpr float kTcLag = 8.f;  // log2 of how far probabilities may pass 1
 constexpr long long kWaitCycles = 4000000000ll;  // a wait gives up after about two seconds
@@ -48,7 +57,7 @@ struct TcShape {
     static constexpr uint32_t kQ = 0;                            // two query tiles
     static constexpr uint32_t kRing = 2 * kTile;
     static constexpr uint32_t kBars = kRing + kSlots * kTile;
-    static constexpr int kNumBars = 2 * kSlots + 8;
+    static constexpr int kNumBars = 2 * kSlots + 9;
     static constexpr uint32_t kTmemPtr = kBars + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemPtr + 4;
     static constexpr uint32_t kSmem = kAbort + 4;
@@ -90,12 +99,17 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return mbar_try(bar, parity) || mbar_wait_long(bar, parity, abort);
 }
 
-// The barrier counts this thread once its copies so far have landed.
-__device__ __forceinline__ void cp_async_report(uint32_t bar)
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
 {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Copies seen through a barrier become visible to the tensor cores' proxy.
+// A box of rows of 64 elements, from column x and row y.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+                 "[%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// This thread's writes to shared memory, visible to the tensor cores' proxy.
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ------------------------------------------------------------- tcgen05
@@ -188,7 +202,8 @@ __device__ __forceinline__ uint32_t tc_off(int r, int c)
 }
 
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const __grid_constant__ PagedParams p)
+__global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap k_map,
+                          const __grid_constant__ CUtensorMap v_map)
 {
     using S = TcShape<D>;
     constexpr int NS = S::kSlots;
@@ -209,20 +224,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     auto s_full = [&](int t) { return bars + 8u * (2 * NS + 1 + t); };
     auto p_full = [&](int t) { return bars + 8u * (2 * NS + 3 + t); };
     auto o_full = [&](int t) { return bars + 8u * (2 * NS + 5 + t); };
-    const uint32_t drained = bars + 8u * (2 * NS + 7);
+    const uint32_t drained = bars + 8u * (2 * NS + 7), clean = bars + 8u * (2 * NS + 8);
 
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
-            mbar_init(full(s), kTcCopyThreads);
+            mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
-        mbar_init(q_full, kTcCopyThreads);
+        mbar_init(q_full, kTcSoftmaxThreads);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
             mbar_init(p_full(t), kTcRows);
             mbar_init(o_full(t), 1);
         }
         mbar_init(drained, 1);
+        mbar_init(clean, 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         proxy_fence();
@@ -249,7 +265,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             visible_keys(p, q, (q.first + t * kTcRows + rows[t] - 1) / p.group, unused, hi[t]);
         }
     }
-    int k_lo = lo[0], k_hi = max(hi[0], hi[1]);
+    int k_lo = lo[0] / kTcKeys * kTcKeys, k_hi = max(hi[0], hi[1]);
     if (p.splits > 1) {
         const long long from = k_lo + (long long)split * p.split_keys;
         if (split + 1 < p.splits)
@@ -266,6 +282,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             first[t] = last[t] = 0;
     }
     const int steps = max(last[0], last[1]);
+    // the last step's first row behind the block's keys: not fetched, or not
+    // of a token; zeroed
+    const int behind = min(k_hi - (k_lo + (steps - 1) * kTcKeys), kTcKeys);
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -292,8 +311,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 };
                 bool go = steps > 0 && mbar_wait(q_full, 0, abort) && mbar_wait(full(0), 0, abort);
                 if (go) {
-                    proxy_fence();
                     tc_fence_after();
+#pragma unroll
                     for (int t = 0; t < 2; ++t)
                         if (in(t, 0))
                             scores(t, 0);
@@ -303,22 +322,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                     const int vt = 2 * i + 1, kt = 2 * i + 2;
                     const int vs = vt % NS, ks = kt % NS;
                     go = mbar_wait(full(vs), (uint32_t)(vt / NS) & 1u, abort);
+                    if (go && i + 1 == steps && behind < kTcKeys)
+                        go = mbar_wait(clean, 0, abort);
                     if (go && i + 1 < steps)
                         go = mbar_wait(full(ks), (uint32_t)(kt / NS) & 1u, abort);
-                    proxy_fence();
-                    for (int t = 0; go && t < 2; ++t) {
-                        if (in(t, i)) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (go && in(t, i)) {
                             go = mbar_wait(p_full(t), (uint32_t)(i - first[t]) & 1u, abort);
-                            if (!go)
-                                break;
-                            tc_fence_after();
-                            products(t, vs, i > first[t]);
-                            if (i + 1 == last[t])
-                                tc_commit(o_full(t));
+                            if (go) {
+                                tc_fence_after();
+                                products(t, vs, i > first[t]);
+                                if (i + 1 == last[t])
+                                    tc_commit(o_full(t));
+                            }
                         }
-                        if (t == 1)
+                        if (go && t == 1)
                             tc_commit(empty(vs));
-                        if (in(t, i + 1))
+                        if (go && in(t, i + 1))
                             scores(t, ks);
                     }
                     if (go && i + 1 < steps)
@@ -332,112 +353,101 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 }
             }
             __syncwarp();
-        } else {
-            // Each thread's copies into a slot report to the slot's barrier
-            // when they land (the issuing thread hands them to the tensor
-            // cores with a proxy fence), so copies for every free slot are
-            // under way at once.
-            const int cw = warp - 9;
-            const int ct = tid - 9 * 32;
-            constexpr int CH = D / 8;          // chunks per row
-            constexpr int RPI = 32 / CH;       // rows per warp instruction
+        } else if (warp == 9) {
+            // Lane e fetches the box of rows e * box of every tile, where there
+            // is one.  Page numbers are read a step ahead.
             const int32_t* table = p.block_table + (int64_t)q.seq * p.table_stride;
-            const uint16_t* kc = p.k_cache + (int64_t)kvh * p.head_stride;
-            const uint16_t* vc = p.v_cache + (int64_t)kvh * p.head_stride;
-            if (steps > 0) {
-                for (int e = ct; e < 2 * kTcRows * CH; e += kTcCopyThreads) {
-                    const int r = e / CH, c = e % CH;
-                    const bool there = r < q.rows;
-                    const int at = q.first + (there ? r : 0), token = at / p.group, head = kvh * p.group + at % p.group;
-                    cp_async16(base + S::kQ + (r >= kTcRows ? S::kTile : 0) + tc_off(r & (kTcRows - 1), c),
-                               p.q + (int64_t)(q.row0 + token) * p.q_row_stride + head * D + c * 8, there);
-                }
-                cp_async_report(q_full);
-            }
-            // A warp copies 44 of a tile's rows (the last one 40), RPI rows per
-            // instruction, CH lanes to a row.  Lane e holds where rows e and
-            // 32 + e of them lie; the page numbers are read a step ahead.
-            // Copying bounded the kernel while each row's place was looked up
-            // and permuted per copy: all that is left per copy is a shuffle
-            // of the offset and one addition (video chunk COPYFIG).
-            constexpr int kOwn = 44;
-            constexpr int kPatterns = 8 / RPI;  // rows of one instruction, modulo 8
-            const int r0 = cw * kOwn, own = min(kOwn, kTcKeys - r0), sub = lane / CH, c = lane % CH;
-            uint32_t dst[kPatterns];
-#pragma unroll
-            for (int e = 0; e < kPatterns; ++e)
-                dst[e] = base + S::kRing + tc_off(r0 + sub + e * RPI, c) - (uint32_t)(e * RPI * 128);
-            int page[2], slot_in[2];
+            const int head_row = kvh * p.head_rows, x = kvh * p.head_cols;
+            const int box = p.box_rows;
+            int page = -1, slot_in = 0, row = 0;
+            bool next = false, there = false;
             auto look_up = [&](int i) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int key = k_lo + i * kTcKeys + r0 + 32 * e + lane;
-                    page[e] = -1;
-                    if (key < k_hi && 32 * e + lane < own) {
-                        const unsigned entry = page_of(p, key);
-                        slot_in[e] = key - (int)entry * p.page_size;
-                        page[e] = __ldg(table + entry);
-                    }
+                const int key = k_lo + i * kTcKeys + lane * box;
+                next = lane * box < kTcKeys && key < k_hi;
+                if (next) {
+                    const unsigned entry = page_of(p, key);
+                    slot_in = key - (int)entry * p.page_size;
+                    page = __ldg(table + entry);
                 }
             };
-            int64_t offs[2];
-            uint32_t there[2];  // bit e: row 32 w + e can be read
-            bool all_there = false;
             if (steps > 0)
                 look_up(0);
-            bool go = true;
-            for (int j = 0; go && j < 2 * steps; ++j) {
+            int j = 0;
+            for (; j < 2 * steps; ++j) {
                 const int slot = j % NS;
                 if ((j & 1) == 0) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const bool ok = page[e] >= 0 && page[e] < p.num_pages;
-                        offs[e] = ok ? (int64_t)page[e] * p.page_stride + (int64_t)slot_in[e] * p.slot_stride : 0;
-                        there[e] = __ballot_sync(0xffffffffu, ok);
-                    }
-                    all_there = there[0] == 0xffffffffu && (there[1] | (own == kOwn ? 0u : 0xf00u)) == 0xfffu;
+                    there = next;
+                    // a page outside the cache: rows outside the map, which read as zeros
+                    row = page >= 0 && page < p.num_pages ? page * p.page_rows + slot_in + head_row : -kTcKeys;
                     if (j / 2 + 1 < steps)
                         look_up(j / 2 + 1);
                 }
-                if (j >= NS) {
-                    const uint32_t parity = (uint32_t)(j / NS - 1) & 1u;
-                    go = __all_sync(0xffffffffu, mbar_wait(empty(slot), parity, abort));
-                    if (!go)
-                        break;
-                }
-                const uint16_t* from = ((j & 1) ? vc : kc) + c * 8;
-                const uint32_t to = slot * S::kTile;
+                if (j >= NS && !__all_sync(0xffffffffu, mbar_wait(empty(slot), (uint32_t)(j / NS - 1) & 1u, abort)))
+                    break;
+                const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, there));
+                if (lane == 0)
+                    mbar_expect(full(slot), boxes * (uint32_t)box * (D * 2));
+                __syncwarp();
+                if (there) {
+                    const uint32_t to = base + S::kRing + slot * S::kTile + (uint32_t)(lane * box) * 128;
 #pragma unroll
-                for (int it = 0; it < kOwn / RPI; ++it) {
-                    const int row = it * RPI;  // of the warp's, plus sub
-                    const int64_t o = __shfl_sync(0xffffffffu, offs[row / 32], (row % 32) + sub);
-                    const uint32_t at = to + dst[it % kPatterns] + (uint32_t)(row * 128);
-                    if (all_there) {
-                        if (row < own)
-                            cp_async16(at, from + o);
-                    } else if (row < own) {
-                        cp_async16(at, from + o, (there[row / 32] >> ((row % 32) + sub)) & 1u);
-                    }
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_box(to + c * kBlockBytes, (j & 1) ? &v_map : &k_map, x + 64 * c, row, full(slot));
                 }
-                cp_async_report(full(slot));
+                __syncwarp();
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
+            // The last tile of v: this warp has seen the slot's previous use end,
+            // so the parity it waits for is the tile's own.
+            if (j == 2 * steps && behind < kTcKeys && steps > 0) {
+                const int slot = (j - 1) % NS;
+                if (__all_sync(0xffffffffu, mbar_wait(full(slot), (uint32_t)((j - 1) / NS) & 1u, abort))) {
+                    for (int c = 0; c < D / 64; ++c)
+                        for (int e = behind * 8 + lane; e < kTcKeys * 8; e += 32)
+                            *reinterpret_cast<uint4*>(smem + S::kRing + slot * S::kTile + c * kBlockBytes + e * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    proxy_fence();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(clean);
+                }
+            }
+            // given up: let the copies under way land before the block ends
+            if (j < 2 * steps && lane == 0) {
+                const long long from = clock64();
+                for (int e = max(j - NS, 0); e < j; ++e)
+                    while (!mbar_try(full(e % NS), (uint32_t)(e / NS) & 1u) && clock64() - from < kWaitCycles) {
+                    }
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        if (steps > 0) {
+            constexpr int CH = D / 8;  // 16-byte chunks per row
+            for (int e = tid; e < 2 * kTcRows * CH; e += kTcSoftmaxThreads) {
+                const int r = e / CH, c = e % CH;
+                const bool there = r < q.rows;
+                const int at = q.first + (there ? r : 0), token = at / p.group, head = kvh * p.group + at % p.group;
+                cp_async16(base + S::kQ + (r >= kTcRows ? S::kTile : 0) + tc_off(r & (kTcRows - 1), c),
+                           p.q + (int64_t)(q.row0 + token) * p.q_row_stride + head * D + c * 8, there);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            proxy_fence();
+            mbar_arrive(q_full);
+        }
         const int t = warp >> 2;
         const int r = tid & (kTcRows - 1);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes: bits 16 and up, times 32
         const uint32_t s_at = tmem + t * kTcKeys + lanes, o_at = tmem + 2 * kTcKeys + t * D + lanes;
-        const bool mine = r < rows[t];
-        const int at = q.first + t * kTcRows + min(r, max(rows[t] - 1, 0));
+        const int have = t ? rows[1] : rows[0];
+        const bool mine = r < have;
+        const int at = q.first + t * kTcRows + min(r, max(have - 1, 0));
         const int token = at / p.group, head = kvh * p.group + at % p.group;
         int r_lo, r_hi;
         visible_keys(p, q, token, r_lo, r_hi);
         r_hi = min(r_hi, k_hi);
         float m = -INFINITY, l = 0.f;
         bool go = true;
-        const int n0 = first[t], n1 = last[t];
+        const int n0 = t ? first[1] : first[0], n1 = t ? last[1] : last[0];
         for (int i = n0; i < n1; ++i) {
             go = mbar_wait(s_full(t), (uint32_t)(i - n0) & 1u, abort);
             go = __all_sync(0xffffffffu, go);
@@ -560,18 +570,79 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int D>
-cudaError_t launch_tc(const PagedParams& p, int tiles, cudaStream_t stream)
+// The cache as rows of one head's elements, slot_stride apart: element x of row
+// g * page_rows + s (+ head_rows per head) is what the caller calls page g,
+// slot s, with a head's columns from h * head_cols.
+bool cache_map(CUtensorMap& map, const PagedParams& p, const uint16_t* cache, int head_dim, int64_t rows, int64_t cols)
 {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<Encode>(fn);
+    }();
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)p.slot_stride * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)p.box_rows}, step[2] = {1, 1};
+    return encode != nullptr &&
+           encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(cache), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_tc(PagedParams p, int tiles, cudaStream_t stream)
+{
+    CacheRows c;
+    CUtensorMap k_map, v_map;
+    if (!cache_rows(p.page_stride, p.slot_stride, p.head_stride, p.num_pages, p.page_size, p.num_kv_heads, D, c))
+        return cudaErrorInvalidValue;
+    p.page_rows = c.page_rows;
+    p.head_rows = c.head_rows;
+    p.head_cols = c.head_cols;
+    p.box_rows = c.box_rows;
+    if (!cache_map(k_map, p, p.k_cache, D, c.rows, c.cols) || !cache_map(v_map, p, p.v_cache, D, c.rows, c.cols))
+        return cudaErrorInvalidValue;
     auto* kernel = paged_attention_tc_kernel<D>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
     if (e != cudaSuccess)
         return e;
     return launch_kernel(kernel, dim3((unsigned)tiles, (unsigned)p.num_kv_heads, (unsigned)p.splits), kTcThreads,
-                         TcShape<D>::kSmem, stream, p);
+                         TcShape<D>::kSmem, stream, p, k_map, v_map);
 }
 
 }  // namespace
+
+bool cache_rows(int64_t page_stride, int64_t slot_stride, int64_t head_stride, int num_pages, int page_size,
+                int num_kv_heads, int head_dim, CacheRows& c)
+{
+    const int64_t pages = num_pages > 0 ? num_pages : 1;
+    if (page_size % 8 != 0)
+        return false;
+    int64_t head_rows = 0, head_cols = 0;
+    if (num_kv_heads > 1) {  // heads lie within a row (slot-major pages) or whole rows apart (head-major)
+        if (head_stride * (num_kv_heads - 1) + head_dim <= slot_stride)
+            head_cols = head_stride;
+        else if (head_stride % slot_stride == 0)
+            head_rows = head_stride / slot_stride;
+        else
+            return false;
+    }
+    if (pages > 1 && page_stride % slot_stride != 0)
+        return false;
+    const int64_t page_rows = pages > 1 ? page_stride / slot_stride : 0;
+    const int64_t rows = (pages - 1) * page_rows + (num_kv_heads - 1) * head_rows + page_size;
+    const int64_t cols = (num_kv_heads - 1) * head_cols + head_dim;
+    if (rows > INT32_MAX || cols > INT32_MAX || slot_stride >= (1ll << 38))
+        return false;
+    const int32_t power = page_size & -page_size;
+    c = CacheRows{(int32_t)page_rows, (int32_t)head_rows, (int32_t)head_cols, power < kTcKeys ? power : kTcKeys, rows, cols};
+    return true;
+}
 
 cudaError_t launch_paged_attention_tc(const PagedParams& p, int tiles, int head_dim, cudaStream_t stream)
 {
