@@ -426,9 +426,20 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
         keys = window + plan.tile_rows;
     const int64_t full = rows * group / plan.tile_rows;
     const int64_t blocks = (full > num_seqs ? full : num_seqs) * num_kv_heads;
-    int64_t splits = (148 * 8 + blocks - 1) / blocks;
-    const int64_t most = (keys + 127) / 128;
-    splits = splits < most ? splits : most;
+    int64_t splits;
+    if (plan.kind == kPagedTc) {
+        // One block per SM.  Splits only fill SMs that would have no block:
+        // each costs its block's start and end (about 9 us, four steps) and the
+        // write and read of its part (a chunk of 1,000 rows of 40 heads over
+        // itself: 59 us whole, 185 in 4 splits), so runs are 512 keys at least.
+        splits = 148 / blocks;
+        const int64_t most = keys / 512;
+        splits = splits < most ? splits : most;
+    } else {
+        splits = (148 * 8 + blocks - 1) / blocks;
+        const int64_t most = (keys + 127) / 128;
+        splits = splits < most ? splits : most;
+    }
     if (splits > 128)
         splits = 128;
     if (splits < 1)

@@ -47,6 +47,7 @@ constexpr int kTcKeys = 128;   // keys per step
 constexpr int kTcThreads = 384;
 constexpr int kTcSoftmaxThreads = 256;
 constexpr uint32_t kBlockBytes = kTcKeys * 128;  // 128 rows of 64 elements
+constexpr int kTcFmaPairs = 0;  // of 8: see exponentials
 constexpr float kTcLag = 8.f;  // log2 of how far probabilities may pass 1
 constexpr long long kWaitCycles = 4000000000ll;  // a wait gives up after about two seconds
 
@@ -57,7 +58,7 @@ struct TcShape {
     static constexpr uint32_t kQ = 0;                            // two query tiles
     static constexpr uint32_t kRing = 2 * kTile;
     static constexpr uint32_t kBars = kRing + kSlots * kTile;
-    static constexpr int kNumBars = 2 * kSlots + 9;
+    static constexpr int kNumBars = 2 * kSlots + 11;
     static constexpr uint32_t kTmemPtr = kBars + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemPtr + 4;
     static constexpr uint32_t kSmem = kAbort + 4;
@@ -111,6 +112,14 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 }
 // This thread's writes to shared memory, visible to the tensor cores' proxy.
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
 
 // ------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -195,6 +204,86 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// 2^t for pairs, on the FMA units.  t = s scale - base with an integer base is
+// rounded to an integer n by adding 1.5 2^23 (the fused product keeps t exact
+// until then), and 2^(t - n), |t - n| <= 1/2, is a polynomial of degree 4 of
+// least relative error there (2.6e-6, from a linear program over a grid of
+// 4001 points; in fp32 2^-18.5); n goes into the exponent.  floor: the s whose
+// t is -125, below which the exponent would leave its range.
+__device__ __forceinline__ f32x2 exp2_fma(f32x2 s, f32x2 scale, float base, float floor)
+{
+    constexpr float kRound = 12582912.f;
+    s.x = fmaxf(s.x, floor);
+    s.y = fmaxf(s.y, floor);
+    const float up = kRound - base;
+    const f32x2 r = f2_fma(s, scale, f2_make(up, up));
+    const f32x2 n = f2_add(r, f2_make(-up, -up));  // n + base
+    const f32x2 f = f2_fma(s, scale, f2_make(-n.x, -n.y));
+    f32x2 y = f2_fma(f, f2_make(0x1.399440p-7f, 0x1.399440p-7f), f2_make(0x1.ca1510p-5f, 0x1.ca1510p-5f));
+    y = f2_fma(f, y, f2_make(0x1.ec06f8p-3f, 0x1.ec06f8p-3f));
+    y = f2_fma(f, y, f2_make(0x1.62e0dap-1f, 0x1.62e0dap-1f));
+    y = f2_fma(f, y, f2_make(0x1.ffffe6p-1f, 0x1.ffffe6p-1f));
+    return f2_make(__int_as_float(__float_as_int(y.x) + (__float_as_int(r.x) << 23)),
+                   __int_as_float(__float_as_int(y.y) + (__float_as_int(r.y) << 23)));
+}
+
+// Probabilities 2^(s scale - base) of 64 scores of a row, to tensor memory as
+// bf16; their sum.  The special-function units make 16 exponentials a cycle
+// and SM, 1024 cycles for a tile, half as long as the step's products take:
+// with FMA, kTcFmaPairs of 8 pairs are computed on the FMA units instead.
+template <bool FMA>
+__device__ __forceinline__ float exponentials(const float* s, float scale, float base, float floor, uint32_t to)
+{
+    const f32x2 scale2 = f2_make(scale, scale), base2 = f2_make(-base, -base);
+    f32x2 sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
+    uint32_t pk[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        const f32x2 x = f2_make(s[2 * c], s[2 * c + 1]);
+        f32x2 e;
+        if (FMA && (c & 7) * kTcFmaPairs % 8 >= 8 - kTcFmaPairs) {
+            e = exp2_fma(x, scale2, base, floor);
+        } else {
+            e = f2_fma(x, scale2, base2);
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+        }
+        sum[c & 1] = f2_add(sum[c & 1], e);
+        pk[c] = f2_to_bf16x2(e);
+    }
+    tc_st32(to, pk);
+    sum[0] = f2_add(sum[0], sum[1]);
+    return sum[0].x + sum[0].y;
+}
+
+// Scores that the row does not see become -inf; their maximum is returned.
+// keys: of the first score, from the row's first and to its last key.
+__device__ __forceinline__ float mask_and_top(float* s, bool clear, int from, int to)
+{
+    if (!clear) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+            if (c < from || c >= to)
+                s[c] = -INFINITY;
+    }
+    float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+    for (int c = 4; c < 64; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            top[e] = c + 4 + e < 64 ? fmaxf(top[e], fmaxf(s[c + e], s[c + 4 + e])) : fmaxf(top[e], s[c + e]);
+    return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+}
+
+__device__ __forceinline__ void hand_over(uint32_t bar)
+{
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+        mbar_arrive(bar);
+}
+
 // Byte offset of 16-byte chunk c of row r in a tile of 128 rows.
 __device__ __forceinline__ uint32_t tc_off(int r, int c)
 {
@@ -222,9 +311,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     auto empty = [&](int s) { return bars + 8u * (NS + s); };
     const uint32_t q_full = bars + 8u * (2 * NS);
     auto s_full = [&](int t) { return bars + 8u * (2 * NS + 1 + t); };
-    auto p_full = [&](int t) { return bars + 8u * (2 * NS + 3 + t); };
-    auto o_full = [&](int t) { return bars + 8u * (2 * NS + 5 + t); };
-    const uint32_t drained = bars + 8u * (2 * NS + 7), clean = bars + 8u * (2 * NS + 8);
+    auto o_full = [&](int t) { return bars + 8u * (2 * NS + 3 + t); };
+    auto p_full = [&](int t, int h) { return bars + 8u * (2 * NS + 5 + 2 * t + h); };
+    const uint32_t drained = bars + 8u * (2 * NS + 9), clean = bars + 8u * (2 * NS + 10);
 
     if (tid == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -234,7 +323,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         mbar_init(q_full, kTcSoftmaxThreads);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), kTcRows);
+            mbar_init(p_full(t, 0), 4);
+            mbar_init(p_full(t, 1), 4);
             mbar_init(o_full(t), 1);
         }
         mbar_init(drained, 1);
@@ -250,7 +340,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S::kTmemPtr);
+    // all 512 columns are the block's own, so its addresses start at 0
+    constexpr uint32_t tmem = 0;
 
     // Keys of the two tiles, the block's share of them, and each tile's steps
     // [first, last) of the block's.
@@ -289,70 +380,87 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
-            if (lane == 0) {
-                constexpr uint32_t kIdescS = TcIdesc<kTcRows, kTcKeys, false>::value;
-                constexpr uint32_t kIdescO = TcIdesc<kTcRows, D, true>::value;
-                auto in = [&](int t, int i) { return i >= first[t] && i < last[t]; };
-                auto scores = [&](int t, int slot) {
-                    const uint32_t a = base + S::kQ + t * S::kTile, b = base + S::kRing + slot * S::kTile;
+            // The whole warp walks the steps and one lane issues: operands
+            // that every lane shares stay in uniform registers.  (With one
+            // lane alone in the loop each product's operands were moved there
+            // first, some 100 cycles per product of 64: MMAFIG.)
+            constexpr uint32_t kIdescS = TcIdesc<kTcRows, kTcKeys, false>::value;
+            constexpr uint32_t kIdescO = TcIdesc<kTcRows, D, true>::value;
+            auto in = [&](int t, int i) { return i >= first[t] && i < last[t]; };
+            auto scores = [&](int t, int slot) {
+                const uint32_t a = base + S::kQ + t * S::kTile, b = base + S::kRing + slot * S::kTile;
+                if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
                         const uint32_t off = (uint32_t)(ks >> 2) * kBlockBytes + (uint32_t)(ks & 3) * 32;
-                        tc_mma_ss(tmem + t * kTcKeys, smem_desc(a + off, 1), smem_desc(b + off, 1), kIdescS, ks > 0);
+                        tc_mma_ss(t * kTcKeys, smem_desc(a + off, 1), smem_desc(b + off, 1), kIdescS, ks > 0);
                     }
                     tc_commit(s_full(t));
-                };
-                auto products = [&](int t, int slot, bool add) {
-                    const uint32_t b = base + S::kRing + slot * S::kTile;
-#pragma unroll
-                    for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                        tc_mma_ts(tmem + 2 * kTcKeys + t * D, tmem + t * kTcKeys + ks * 8,
-                                  smem_desc(b + ks * 2048, kBlockBytes >> 4), kIdescO, add || ks > 0);
-                };
-                bool go = steps > 0 && mbar_wait(q_full, 0, abort) && mbar_wait(full(0), 0, abort);
-                if (go) {
-                    tc_fence_after();
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        if (in(t, 0))
-                            scores(t, 0);
-                    tc_commit(empty(0));
                 }
-                for (int i = 0; go && i < steps; ++i) {
-                    const int vt = 2 * i + 1, kt = 2 * i + 2;
-                    const int vs = vt % NS, ks = kt % NS;
-                    go = mbar_wait(full(vs), (uint32_t)(vt / NS) & 1u, abort);
-                    if (go && i + 1 == steps && behind < kTcKeys)
-                        go = mbar_wait(clean, 0, abort);
-                    if (go && i + 1 < steps)
-                        go = mbar_wait(full(ks), (uint32_t)(kt / NS) & 1u, abort);
+                __syncwarp();
+            };
+            auto products = [&](int t, int slot, int h, bool add) {
+                const uint32_t b = base + S::kRing + slot * S::kTile;
+                if (elect_one()) {
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (go && in(t, i)) {
-                            go = mbar_wait(p_full(t), (uint32_t)(i - first[t]) & 1u, abort);
-                            if (go) {
-                                tc_fence_after();
-                                products(t, vs, i > first[t]);
-                                if (i + 1 == last[t])
-                                    tc_commit(o_full(t));
-                            }
-                        }
-                        if (go && t == 1)
-                            tc_commit(empty(vs));
-                        if (go && in(t, i + 1))
-                            scores(t, ks);
-                    }
-                    if (go && i + 1 < steps)
-                        tc_commit(empty(ks));
+                    for (int ks = h * (kTcKeys / 32); ks < (h + 1) * (kTcKeys / 32); ++ks)
+                        tc_mma_ts(2 * kTcKeys + t * D, t * kTcKeys + ks * 8, smem_desc(b + ks * 2048, kBlockBytes >> 4),
+                                  kIdescO, add || ks > 0);
                 }
-                if (!go && steps > 0) {  // given up: let what was issued end before the memory is freed
-                    tc_commit(drained);
-                    const long long from = clock64();
-                    while (!mbar_try(drained, 0) && clock64() - from < kWaitCycles) {
-                    }
-                }
+                __syncwarp();
+            };
+            auto commit = [&](uint32_t bar) {
+                if (elect_one())
+                    tc_commit(bar);
+                __syncwarp();
+            };
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+            };
+            bool go = steps > 0 && wait(q_full, 0) && wait(full(0), 0);
+            if (go) {
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (in(t, 0))
+                        scores(t, 0);
+                commit(empty(0));
             }
-            __syncwarp();
+            for (int i = 0; go && i < steps; ++i) {
+                const int vt = 2 * i + 1, kt = 2 * i + 2;
+                const int vs = vt % NS, ks = kt % NS;
+                go = wait(full(vs), (uint32_t)(vt / NS) & 1u);
+                if (go && i + 1 == steps && behind < kTcKeys)
+                    go = wait(clean, 0);
+                if (go && i + 1 < steps)
+                    go = wait(full(ks), (uint32_t)(kt / NS) & 1u);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (go && in(t, i)) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (go && (go = wait(p_full(t, h), (uint32_t)(i - first[t]) & 1u))) {
+                                tc_fence_after();
+                                products(t, vs, h, i > first[t]);
+                            }
+                        if (go && i + 1 == last[t])
+                            commit(o_full(t));
+                    }
+                    if (go && t == 1)
+                        commit(empty(vs));
+                    if (go && in(t, i + 1))
+                        scores(t, ks);
+                }
+                if (go && i + 1 < steps)
+                    commit(empty(ks));
+            }
+            if (!go && steps > 0) {  // given up: let what was issued end before the memory is freed
+                commit(drained);
+                const long long from = clock64();
+                while (!mbar_try(drained, 0) && clock64() - from < kWaitCycles) {
+                }
+                __syncwarp();
+            }
         } else if (warp == 9) {
             // Lane e fetches the box of rows e * box of every tile, where there
             // is one.  Page numbers are read a step ahead.
@@ -446,6 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         visible_keys(p, q, token, r_lo, r_hi);
         r_hi = min(r_hi, k_hi);
         float m = -INFINITY, l = 0.f;
+        const float inv_scale = 1.f / p.scale_log2;
         bool go = true;
         const int n0 = t ? first[1] : first[0], n1 = t ? last[1] : last[0];
         for (int i = n0; i < n1; ++i) {
@@ -454,66 +563,54 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             if (!go)
                 break;
             tc_fence_after();
-            float s[kTcKeys];
-#pragma unroll
-            for (int c = 0; c < kTcKeys; c += 32)
-                tc_ld32(s_at + c, s + c);
-            tc_wait_ld();
-#pragma unroll
-            for (int c = 0; c < kTcKeys; c += 32)
-                tc_tie32(s + c);
+            // The exponentials take the last step's m, before this step's
+            // maximum is known; a maximum that has outgrown it (the first
+            // step's always has) brings the sums up to date and repeats the
+            // first half, which is handed over only then.
             const int k0 = k_lo + i * kTcKeys;
-            if (!__all_sync(0xffffffffu, r_lo <= k0 && r_hi >= k0 + kTcKeys)) {
-#pragma unroll
-                for (int c = 0; c < kTcKeys; ++c)
-                    if (k0 + c < r_lo || k0 + c >= r_hi)
-                        s[c] = -INFINITY;
-            }
-            float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-            for (int c = 4; c < kTcKeys; ++c)
-                top[c & 3] = fmaxf(top[c & 3], s[c]);
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale_log2;
-            if (i == n0) {
-                m = mx;
-            } else if (__any_sync(0xffffffffu, mx > m + kTcLag)) {
-                const float mn = mx > m + kTcLag ? mx : m;
+            const bool clear = __all_sync(0xffffffffu, r_lo <= k0 && r_hi >= k0 + kTcKeys);
+            float s[kTcKeys];
+            tc_ld32(s_at, s);
+            tc_ld32(s_at + 32, s + 32);
+            tc_wait_ld();
+            tc_tie32(s);
+            tc_tie32(s + 32);
+            tc_ld32(s_at + 64, s + 64);
+            tc_ld32(s_at + 96, s + 96);
+            float mx = mask_and_top(s, clear, r_lo - k0, r_hi - k0);
+            float base_m = m == -INFINITY ? 0.f : m;
+            float part = clear ? exponentials<true>(s, p.scale_log2, base_m, (base_m - 125.f) * inv_scale, s_at)
+                               : exponentials<false>(s, p.scale_log2, base_m, 0.f, s_at);
+            tc_wait_ld();
+            tc_tie32(s + 64);
+            tc_tie32(s + 96);
+            mx = fmaxf(mx, mask_and_top(s + 64, clear, r_lo - k0 - 64, r_hi - k0 - 64)) * p.scale_log2;
+            if (__any_sync(0xffffffffu, mx > m + kTcLag)) {
+                const float mn = mx > m + kTcLag ? ceilf(mx) : m;
                 const float f = m == mn ? 1.f : ex2(m - mn);  // -inf stays -inf until a key is seen
                 m = mn;
+                base_m = m == -INFINITY ? 0.f : m;
                 l *= f;
+                if (i > n0) {
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float o[32];
-                    tc_ld32(o_at + c, o);
-                    tc_wait_ld();
-                    tc_tie32(o);
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        tc_ld32(o_at + c, o);
+                        tc_wait_ld();
+                        tc_tie32(o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] *= f;
-                    tc_st32(o_at + c, reinterpret_cast<const uint32_t*>(o));
+                        for (int e = 0; e < 32; ++e)
+                            o[e] *= f;
+                        tc_st32(o_at + c, reinterpret_cast<const uint32_t*>(o));
+                    }
                 }
+                part = exponentials<false>(s, p.scale_log2, base_m, 0.f, s_at);
             }
-            const float base_m = m == -INFINITY ? 0.f : m;
-            const f32x2 scale2 = f2_make(p.scale_log2, p.scale_log2), base2 = f2_make(-base_m, -base_m);
-            f32x2 sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    f32x2 e = f2_fma(f2_make(s[64 * h + 2 * c], s[64 * h + 2 * c + 1]), scale2, base2);
-                    e.x = ex2(e.x);
-                    e.y = ex2(e.y);
-                    sum[c & 1] = f2_add(sum[c & 1], e);
-                    pk[c] = f2_to_bf16x2(e);
-                }
-                tc_st32(s_at + 32 * h, pk);
-            }
-            sum[0] = f2_add(sum[0], sum[1]);
-            l += sum[0].x + sum[0].y;
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(p_full(t));
+            hand_over(p_full(t, 0));
+            part += clear ? exponentials<true>(s + 64, p.scale_log2, base_m, (base_m - 125.f) * inv_scale, s_at + 32)
+                          : exponentials<false>(s + 64, p.scale_log2, base_m, 0.f, s_at + 32);
+            l += part;
+            hand_over(p_full(t, 1));
         }
         if (go && n1 > n0) {
             go = mbar_wait(o_full(t), 0, abort);
