@@ -28,7 +28,7 @@
 // Steps begin at multiples of 128 keys, so boxes keep their alignment.
 // The two tiles alternate: while one's softmax runs, the other's products do.
 // Tensor memory (512 columns of 128 lanes x 32 bits): s0, s1 (128 each), o0,
-// o1 (D each); p takes the first half of its s, once the row is in registers.
+// o1 (D each); p takes the second half of its s, once the row is in registers.
 // The products of one tile are issued in the order o(i), s(i+1), and a
 // commit covers everything issued before it, so "s(i+1) is there" also says
 // that o(i) is complete and p(i) is free.
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = h * (kTcKeys / 32); ks < (h + 1) * (kTcKeys / 32); ++ks)
-                        tc_mma_ts(2 * kTcKeys + t * D, t * kTcKeys + ks * 8, smem_desc(b + ks * 2048, kBlockBytes >> 4),
+                        tc_mma_ts(2 * kTcKeys + t * D, t * kTcKeys + kTcKeys / 2 + ks * 8, smem_desc(b + ks * 2048, kBlockBytes >> 4),
                                   kIdescO, add || ks > 0);
                 }
                 __syncwarp();
@@ -546,6 +546,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         const int r = tid & (kTcRows - 1);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes: bits 16 and up, times 32
         const uint32_t s_at = tmem + t * kTcKeys + lanes, o_at = tmem + 2 * kTcKeys + t * D + lanes;
+        const uint32_t p_at = s_at + kTcKeys / 2;
         const int have = t ? rows[1] : rows[0];
         const bool mine = r < have;
         const int at = q.first + t * kTcRows + min(r, max(have - 1, 0));
@@ -570,21 +571,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             const int k0 = k_lo + i * kTcKeys;
             const bool clear = __all_sync(0xffffffffu, r_lo <= k0 && r_hi >= k0 + kTcKeys);
             float s[kTcKeys];
-            tc_ld32(s_at, s);
-            tc_ld32(s_at + 32, s + 32);
+#pragma unroll
+            for (int c = 0; c < kTcKeys; c += 32)
+                tc_ld32(s_at + c, s + c);
             tc_wait_ld();
-            tc_tie32(s);
-            tc_tie32(s + 32);
-            tc_ld32(s_at + 64, s + 64);
-            tc_ld32(s_at + 96, s + 96);
-            float mx = mask_and_top(s, clear, r_lo - k0, r_hi - k0);
+#pragma unroll
+            for (int c = 0; c < kTcKeys; c += 32)
+                tc_tie32(s + c);
+            float mx = fmaxf(mask_and_top(s, clear, r_lo - k0, r_hi - k0),
+                             mask_and_top(s + 64, clear, r_lo - k0 - 64, r_hi - k0 - 64)) * p.scale_log2;
             float base_m = m == -INFINITY ? 0.f : m;
-            float part = clear ? exponentials<true>(s, p.scale_log2, base_m, (base_m - 125.f) * inv_scale, s_at)
-                               : exponentials<false>(s, p.scale_log2, base_m, 0.f, s_at);
-            tc_wait_ld();
-            tc_tie32(s + 64);
-            tc_tie32(s + 96);
-            mx = fmaxf(mx, mask_and_top(s + 64, clear, r_lo - k0 - 64, r_hi - k0 - 64)) * p.scale_log2;
+            float part = clear ? exponentials<true>(s, p.scale_log2, base_m, (base_m - 125.f) * inv_scale, p_at)
+                               : exponentials<false>(s, p.scale_log2, base_m, 0.f, p_at);
             if (__any_sync(0xffffffffu, mx > m + kTcLag)) {
                 const float mn = mx > m + kTcLag ? ceilf(mx) : m;
                 const float f = m == mn ? 1.f : ex2(m - mn);  // -inf stays -inf until a key is seen
@@ -604,11 +602,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                         tc_st32(o_at + c, reinterpret_cast<const uint32_t*>(o));
                     }
                 }
-                part = exponentials<false>(s, p.scale_log2, base_m, 0.f, s_at);
+                float again[64];  // the first half's scores: p has only taken the second half's place
+                tc_ld32(s_at, again);
+                tc_ld32(s_at + 32, again + 32);
+                tc_wait_ld();
+                tc_tie32(again);
+                tc_tie32(again + 32);
+                mask_and_top(again, clear, r_lo - k0, r_hi - k0);
+                part = exponentials<false>(again, p.scale_log2, base_m, 0.f, p_at);
             }
             hand_over(p_full(t, 0));
-            part += clear ? exponentials<true>(s + 64, p.scale_log2, base_m, (base_m - 125.f) * inv_scale, s_at + 32)
-                          : exponentials<false>(s + 64, p.scale_log2, base_m, 0.f, s_at + 32);
+            part += clear ? exponentials<true>(s + 64, p.scale_log2, base_m, (base_m - 125.f) * inv_scale, p_at + 32)
+                          : exponentials<false>(s + 64, p.scale_log2, base_m, 0.f, p_at + 32);
             l += part;
             hand_over(p_full(t, 1));
         }
