@@ -30,8 +30,9 @@ __device__ __forceinline__ bool map_query_tile(int t, const PagedParams& p, int 
     int before = 0;
     for (int base = 0; base < p.pk.num_seqs; base += kWarp) {
         const int b = base + lane;
-        int n = 0, tiles = 0, c0 = 0, row0 = 0;
+        int n = 0, tiles = 0, c0 = 0, row0 = 0, kv = 0;
         if (b < p.pk.num_seqs) {
+            kv = __ldg(p.kv_lens + b);
             c0 = __ldg(p.pk.cu_seqlens + b);
             row0 = __ldg(p.pk.cu_seqlens_padded + b);
             n = min(__ldg(p.pk.cu_seqlens + b + 1) - c0, __ldg(p.pk.cu_seqlens_padded + b + 1) - row0);
@@ -58,7 +59,7 @@ __device__ __forceinline__ bool map_query_tile(int t, const PagedParams& p, int 
             q.ordinal0 = __shfl_sync(0xffffffffu, c0, l);
             q.first = (t - before - excl) * R;
             q.rows = min(R, q.n * p.group - q.first);
-            q.kv_len = max(__ldg(p.kv_lens + q.seq), 0);
+            q.kv_len = max(__shfl_sync(0xffffffffu, kv, l), 0);
             q.kv_end = (int)min((long long)q.kv_len, (long long)p.max_pages * p.page_size);
             return true;
         }

@@ -47,7 +47,6 @@ constexpr int kTcKeys = 128;   // keys per step
 constexpr int kTcThreads = 384;
 constexpr int kTcSoftmaxThreads = 256;
 constexpr uint32_t kBlockBytes = kTcKeys * 128;  // 128 rows of 64 elements
-constexpr int kTcFmaPairs = 0;  // of 8: see exponentials
 constexpr float kTcLag = 8.f;  // log2 of how far probabilities may pass 1
 constexpr long long kWaitCycles = 4000000000ll;  // a wait gives up after about two seconds
 
@@ -204,50 +203,21 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// 2^t for pairs, on the FMA units.  t = s scale - base with an integer base is
-// rounded to an integer n by adding 1.5 2^23 (the fused product keeps t exact
-// until then), and 2^(t - n), |t - n| <= 1/2, is a polynomial of degree 4 of
-// least relative error there (2.6e-6, from a linear program over a grid of
-// 4001 points; in fp32 2^-18.5); n goes into the exponent.  floor: the s whose
-// t is -125, below which the exponent would leave its range.
-__device__ __forceinline__ f32x2 exp2_fma(f32x2 s, f32x2 scale, float base, float floor)
-{
-    constexpr float kRound = 12582912.f;
-    s.x = fmaxf(s.x, floor);
-    s.y = fmaxf(s.y, floor);
-    const float up = kRound - base;
-    const f32x2 r = f2_fma(s, scale, f2_make(up, up));
-    const f32x2 n = f2_add(r, f2_make(-up, -up));  // n + base
-    const f32x2 f = f2_fma(s, scale, f2_make(-n.x, -n.y));
-    f32x2 y = f2_fma(f, f2_make(0x1.399440p-7f, 0x1.399440p-7f), f2_make(0x1.ca1510p-5f, 0x1.ca1510p-5f));
-    y = f2_fma(f, y, f2_make(0x1.ec06f8p-3f, 0x1.ec06f8p-3f));
-    y = f2_fma(f, y, f2_make(0x1.62e0dap-1f, 0x1.62e0dap-1f));
-    y = f2_fma(f, y, f2_make(0x1.ffffe6p-1f, 0x1.ffffe6p-1f));
-    return f2_make(__int_as_float(__float_as_int(y.x) + (__float_as_int(r.x) << 23)),
-                   __int_as_float(__float_as_int(y.y) + (__float_as_int(r.y) << 23)));
-}
-
 // Probabilities 2^(s scale - base) of 64 scores of a row, to tensor memory as
 // bf16; their sum.  The special-function units make 16 exponentials a cycle
-// and SM, 1024 cycles for a tile, half as long as the step's products take:
-// with FMA, kTcFmaPairs of 8 pairs are computed on the FMA units instead.
-template <bool FMA>
-__device__ __forceinline__ float exponentials(const float* s, float scale, float base, float floor, uint32_t to)
+// and SM: 1024 cycles for a tile.  (A polynomial on the FMA units for 1 to 5 of
+// 8 pairs made the kernel slower, 2352 us -> 2420 for 1 of 8: its instructions
+// cost what they save.)
+__device__ __forceinline__ float exponentials(const float* s, float scale, float base, uint32_t to)
 {
     const f32x2 scale2 = f2_make(scale, scale), base2 = f2_make(-base, -base);
     f32x2 sum[2] = {f2_make(0.f, 0.f), f2_make(0.f, 0.f)};
     uint32_t pk[32];
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
-        const f32x2 x = f2_make(s[2 * c], s[2 * c + 1]);
-        f32x2 e;
-        if (FMA && (c & 7) * kTcFmaPairs % 8 >= 8 - kTcFmaPairs) {
-            e = exp2_fma(x, scale2, base, floor);
-        } else {
-            e = f2_fma(x, scale2, base2);
-            e.x = ex2(e.x);
-            e.y = ex2(e.y);
-        }
+        f32x2 e = f2_fma(f2_make(s[2 * c], s[2 * c + 1]), scale2, base2);
+        e.x = ex2(e.x);
+        e.y = ex2(e.y);
         sum[c & 1] = f2_add(sum[c & 1], e);
         pk[c] = f2_to_bf16x2(e);
     }
@@ -316,6 +286,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     const uint32_t drained = bars + 8u * (2 * NS + 9), clean = bars + 8u * (2 * NS + 10);
 
     if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
         for (int s = 0; s < NS; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
@@ -529,19 +501,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        if (steps > 0) {
-            constexpr int CH = D / 8;  // 16-byte chunks per row
-            for (int e = tid; e < 2 * kTcRows * CH; e += kTcSoftmaxThreads) {
-                const int r = e / CH, c = e % CH;
-                const bool there = r < q.rows;
-                const int at = q.first + (there ? r : 0), token = at / p.group, head = kvh * p.group + at % p.group;
-                cp_async16(base + S::kQ + (r >= kTcRows ? S::kTile : 0) + tc_off(r & (kTcRows - 1), c),
-                           p.q + (int64_t)(q.row0 + token) * p.q_row_stride + head * D + c * 8, there);
-            }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            proxy_fence();
-            mbar_arrive(q_full);
-        }
         const int t = warp >> 2;
         const int r = tid & (kTcRows - 1);
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // the warp's 32 lanes: bits 16 and up, times 32
@@ -551,11 +510,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         const bool mine = r < have;
         const int at = q.first + t * kTcRows + min(r, max(have - 1, 0));
         const int token = at / p.group, head = kvh * p.group + at % p.group;
+        if (steps > 0) {
+            // a warp copies the queries of its own 32 rows, RPI rows at a time
+            constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte chunks per row, rows per instruction
+            const int64_t mine_at = (int64_t)(q.row0 + token) * p.q_row_stride + head * D;
+            const uint32_t there = __ballot_sync(0xffffffffu, mine);
+            const uint32_t to = base + S::kQ + t * S::kTile;
+#pragma unroll
+            for (int e = 0; e < 32; e += RPI) {
+                const int row = e + lane / CH, c = lane % CH;
+                const int64_t from = __shfl_sync(0xffffffffu, mine_at, row);
+                cp_async16(to + tc_off((r & ~31) + row, c), p.q + from + c * 8, (there >> row) & 1u);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            proxy_fence();
+            mbar_arrive(q_full);
+        }
         int r_lo, r_hi;
         visible_keys(p, q, token, r_lo, r_hi);
         r_hi = min(r_hi, k_hi);
         float m = -INFINITY, l = 0.f;
-        const float inv_scale = 1.f / p.scale_log2;
         bool go = true;
         const int n0 = t ? first[1] : first[0], n1 = t ? last[1] : last[0];
         for (int i = n0; i < n1; ++i) {
@@ -581,10 +555,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             float mx = fmaxf(mask_and_top(s, clear, r_lo - k0, r_hi - k0),
                              mask_and_top(s + 64, clear, r_lo - k0 - 64, r_hi - k0 - 64)) * p.scale_log2;
             float base_m = m == -INFINITY ? 0.f : m;
-            float part = clear ? exponentials<true>(s, p.scale_log2, base_m, (base_m - 125.f) * inv_scale, p_at)
-                               : exponentials<false>(s, p.scale_log2, base_m, 0.f, p_at);
+            float part = exponentials(s, p.scale_log2, base_m, p_at);
             if (__any_sync(0xffffffffu, mx > m + kTcLag)) {
-                const float mn = mx > m + kTcLag ? ceilf(mx) : m;
+                const float mn = mx > m + kTcLag ? mx : m;
                 const float f = m == mn ? 1.f : ex2(m - mn);  // -inf stays -inf until a key is seen
                 m = mn;
                 base_m = m == -INFINITY ? 0.f : m;
@@ -609,11 +582,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 tc_tie32(again);
                 tc_tie32(again + 32);
                 mask_and_top(again, clear, r_lo - k0, r_hi - k0);
-                part = exponentials<false>(again, p.scale_log2, base_m, 0.f, p_at);
+                part = exponentials(again, p.scale_log2, base_m, p_at);
             }
             hand_over(p_full(t, 0));
-            part += clear ? exponentials<true>(s + 64, p.scale_log2, base_m, (base_m - 125.f) * inv_scale, p_at + 32)
-                          : exponentials<false>(s + 64, p.scale_log2, base_m, 0.f, p_at + 32);
+            part += exponentials(s + 64, p.scale_log2, base_m, p_at + 32);
             l += part;
             hand_over(p_full(t, 1));
         }
