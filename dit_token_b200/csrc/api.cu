@@ -674,7 +674,7 @@ dit_status dit_paged_attention(const void* q, int64_t q_row_stride, const void* 
     p.kv_lens = kv_lens;
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) +
-                                          num_rows_padded * num_q_heads * plan.splits * head_dim * 4);
+                                          plan.part_rows * head_dim * 4);
     p.q_row_stride = q_row_stride;
     p.out_row_stride = out_row_stride;
     p.page_stride = page_stride;

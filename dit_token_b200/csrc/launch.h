@@ -221,6 +221,7 @@ struct PagedPlan {
     int tiles;       // upper bound of the batch's query tiles
     int splits;
     int split_keys;
+    int64_t part_rows;   // rows of partial sums in the workspace
     int64_t bytes;       // workspace of this call
     int64_t most_bytes;  // of any window and shorter key axis at these sizes
 };
@@ -229,6 +230,8 @@ struct PagedPlan {
 bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int64_t max_chunk,
                 int64_t max_kv_len, int64_t window, bool regular, PagedPlan& plan);
 cudaError_t launch_paged_attention_tc(const PagedParams& p, int tiles, int head_dim, cudaStream_t stream);
+int64_t paged_narrow_slots(int head_dim);  // rows of partial sums it wants
+cudaError_t launch_paged_attention_narrow(const PagedParams& p, int head_dim, cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedParams& p, const PagedPlan& plan, int head_dim, cudaStream_t stream);
 
 cudaError_t launch_rope_cache(const RopeCacheParams& p, int head_dim, int rope_mode, cudaStream_t stream);

@@ -10,45 +10,18 @@
 // lse = -inf.
 //
 // The rows of a tile are the (token, head) pairs that share a key head, so
-// grouped heads read each key once.  Two shapes:
-//   narrow  16 rows, 4 warps that take a quarter of each key tile: next tokens
-//           and chunks of a few rows; bound by reading the cache (HBM);
-//   wide    64 rows, 16 per warp, every warp over all keys of a tile: head
-//           sizes and chunks the tensor-memory kernel does not take.
+// grouped heads read each key once.  A block takes 64 of them, 16 per warp,
+// and every warp all keys of a tile.  This is the kernel of the chunks that the
+// tensor-memory kernel does not take (heads of 256; caches whose strides or
+// page size TMA cannot follow); paged_attention_narrow.cu is that of next
+// tokens.
 // Key and value tiles arrive by 16-byte asynchronous copies, which take any
 // page size and stride and write zeros for keys that are not there; STAGES
 // tiles are in flight.
-#include "paged.cuh"
+#include "paged_mma.cuh"
 
 namespace dit {
 namespace {
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4])
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4])
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Byte offset of 16-byte chunk c of row r in a tile of rows of D elements:
-// chunks are permuted within each row by the row's low bits, so that the 8
-// rows an ldmatrix reads at one column lie in different banks.
-template <int D>
-__device__ __forceinline__ uint32_t tile_off(int r, int c)
-{
-    return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
-}
 
 template <int D, int WM, int WN, int BN, int STAGES>
 struct Shape {
@@ -395,8 +368,7 @@ template <int D>
 cudaError_t launch_d(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream)
 {
     const cudaError_t e = plan.kind == kPagedTc ? launch_paged_attention_tc(p, plan.tiles, D, stream)
-                          : plan.kind == kPagedNarrow ? launch_shape<D, 1, 4, 64, D == 256 ? 2 : 3>(p, plan.tiles, stream)
-                                                    : launch_shape<D, 4, 1, 64, D == 256 ? 2 : 3>(p, plan.tiles, stream);
+                                                : launch_shape<D, 4, 1, 64, D == 256 ? 2 : 3>(p, plan.tiles, stream);
     if (e != cudaSuccess || p.splits == 1)
         return e;
     const long long warps = (long long)p.pk.num_rows_padded * p.num_q_heads;
@@ -411,8 +383,16 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
 {
     const int64_t group = num_q_heads / num_kv_heads;
     const int64_t chunk = max_chunk > 0 && max_chunk < rows ? max_chunk : rows;
-    plan.kind = chunk * group <= 32 ? kPagedNarrow : (head_dim == 256 || !regular ? kPagedWide : kPagedTc);
-    plan.tile_rows = plan.kind == kPagedNarrow ? 16 : (plan.kind == kPagedWide ? 64 : 256);
+    plan = PagedPlan{};
+    if (chunk * group <= 32) {
+        plan.kind = kPagedNarrow;
+        plan.splits = 1;
+        plan.part_rows = paged_narrow_slots(head_dim);
+        plan.bytes = plan.most_bytes = plan.part_rows * (head_dim * 4 + 8);
+        return true;
+    }
+    plan.kind = head_dim == 256 || !regular ? kPagedWide : kPagedTc;
+    plan.tile_rows = plan.kind == kPagedWide ? 64 : 256;
     // ceil over each sequence adds at most one tile per sequence
     const int64_t tiles = rows * group / plan.tile_rows + (num_seqs < rows ? num_seqs : rows);
     if (tiles > INT32_MAX)
@@ -454,12 +434,15 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
     splits = (keys + run - 1) / run;
     plan.splits = (int)(splits < 1 ? 1 : splits);
     plan.split_keys = (int)(run > INT32_MAX ? INT32_MAX : run);
+    plan.part_rows = rows * num_q_heads * plan.splits;
     plan.bytes = plan.splits == 1 ? 0 : part * plan.splits;
     return true;
 }
 
 cudaError_t launch_paged_attention(const PagedParams& p, const PagedPlan& plan, int head_dim, cudaStream_t stream)
 {
+    if (plan.kind == kPagedNarrow)
+        return launch_paged_attention_narrow(p, head_dim, stream);
     switch (head_dim) {
     case 64: return launch_d<64>(p, plan, stream);
     case 128: return launch_d<128>(p, plan, stream);
