@@ -5,7 +5,7 @@
 // cached key and value once and computes little with each: it is bound by
 // HBM, as long as every SM reads all the time.  Requests' caches differ
 // in length by orders of magnitude, so the key axis is not cut per request:
-// the key tiles (64 keys) of all (sequence, 16-row tile, key head) triples
+// the key tiles of all (sequence, 16-row tile, key head) triples
 // are numbered through, and each block takes an equal run of that list,
 // whatever it crosses.  The lengths are read on the device, so a captured
 // call keeps its balance as caches grow.  A triple that lies within one run is
@@ -15,32 +15,37 @@
 // run has at most one part that began before it and one that goes on behind
 // it, so two slots per block are the whole workspace.
 //
-// A block: 4 warps share 16 rows and take 16 keys each of a tile; STAGES tiles
-// are under way by 16-byte asynchronous copies, which take any page size and
-// stride and write zeros for keys that are not there.
+// A block's warps share 16 rows and part each tile's keys; the next tile is
+// under way by 16-byte asynchronous copies, which take any page size and
+// stride and write zeros for keys that are not there.  (TMA boxes took 185
+// against 153 us for heads of 64, whose rows are 128 bytes in a slot-major
+// cache, and 249 against 239 for 128.)
 #include "paged_mma.cuh"
 
 namespace dit {
 namespace {
 
 constexpr int kNRows = 16;
-constexpr int kNKeys = 64;
-constexpr int kNWarps = 4;
-constexpr int kNThreads = 32 * kNWarps;
 
 template <int D>
 struct NShape {
-    static constexpr int kStages = D == 256 ? 2 : 3;
-    static constexpr int kPerSm = D == 256 ? 1 : (D == 128 ? 2 : 4);  // blocks
+    // A stage is 32 KB of keys and values (D 64, 128 and 256: 128, 64 and 32
+    // keys), 16 keys per warp and more where a row is short; two stages and
+    // three blocks per SM.  NFIG
+    static constexpr int kWarps = D == 256 ? 2 : 4;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kKeys = 8192 / D;
+    static constexpr int kStages = 2;
+    static constexpr int kPerSm = 3;  // blocks
     static constexpr int kBlocks = 148 * kPerSm;
-    static constexpr int kTile = kNKeys * D * 2;
+    static constexpr int kTile = kKeys * D * 2;
     static constexpr int kQ = kNRows * D * 2;
     static constexpr int kRing = 2 * kStages * kTile;
     static constexpr int kOStride = D + 4;
-    static constexpr int kO = kNWarps * kNRows * kOStride * 4;
+    static constexpr int kO = kWarps * kNRows * kOStride * 4;
     static constexpr int kMain = kRing > kO ? kRing : kO;
-    static constexpr int kOffs = 2 * kNKeys * 8;
-    static constexpr int kSmem = kQ + kMain + kOffs + kNWarps * kNRows * 8;
+    static constexpr int kOffs = 2 * kKeys * 8;
+    static constexpr int kSmem = kQ + kMain + kOffs + kWarps * kNRows * 8;
 };
 
 // A sequence in the list: its tiles of 16 rows and, for each of them and each
@@ -55,6 +60,7 @@ struct Listed {
     }
 };
 
+template <int D>
 __device__ __forceinline__ Listed list_seq(const PagedParams& p, int b)
 {
     Listed s{};
@@ -77,7 +83,7 @@ __device__ __forceinline__ Listed list_seq(const PagedParams& p, int b)
     int hi, unused;
     visible_keys(p, q, 0, s.lo, unused);
     visible_keys(p, q, s.n - 1, unused, hi);
-    s.k_tiles = hi > s.lo ? (hi - s.lo + kNKeys - 1) / kNKeys : 1;
+    s.k_tiles = hi > s.lo ? (hi - s.lo + NShape<D>::kKeys - 1) / NShape<D>::kKeys : 1;
     return s;
 }
 
@@ -88,12 +94,13 @@ __device__ __forceinline__ long long shfl_ll(long long v, int src)
 
 // Warp-collective: the list's entries before sequence `until` (all of it for
 // num_seqs).
+template <int D>
 __device__ __forceinline__ long long listed_before(const PagedParams& p, int until, int lane)
 {
     long long sum = 0;
     for (int base = 0; base < until; base += kWarp)
         if (base + lane < until)
-            sum += list_seq(p, base + lane).count(p);
+            sum += list_seq<D>(p, base + lane).count(p);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1)
         sum += (long long)__shfl_xor_sync(0xffffffffu, (unsigned long long)sum, o);
@@ -102,11 +109,12 @@ __device__ __forceinline__ long long listed_before(const PagedParams& p, int unt
 
 // Warp-collective: the sequence that holds entry `at` (0 <= at < the list's
 // length), and the entries before it.
+template <int D>
 __device__ __forceinline__ int find_listed(const PagedParams& p, long long at, int lane, long long& before)
 {
     before = 0;
     for (int base = 0; base < p.pk.num_seqs; base += kWarp) {
-        const long long c = list_seq(p, base + lane).count(p);
+        const long long c = list_seq<D>(p, base + lane).count(p);
         long long sum = c;
 #pragma unroll
         for (int o = 1; o < kWarp; o <<= 1) {
@@ -134,14 +142,15 @@ __device__ __forceinline__ long long run_length(long long total)
 }
 
 template <int D>
-__global__ void __launch_bounds__(kNThreads) paged_narrow_kernel(const __grid_constant__ PagedParams p)
+__global__ void __launch_bounds__(NShape<D>::kThreads) paged_narrow_kernel(const __grid_constant__ PagedParams p)
 {
     using S = NShape<D>;
-    constexpr int NK = kNKeys / kNWarps, CH = D / 8, ST = S::kStages;
+    constexpr int kKeys = S::kKeys, kNWarps = S::kWarps, kNThreads = S::kThreads;
+    constexpr int NK = kKeys / kNWarps, CH = D / 8, ST = S::kStages;
     extern __shared__ __align__(128) unsigned char smem[];
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long total = listed_before(p, p.pk.num_seqs, lane);
+    const long long total = listed_before<D>(p, p.pk.num_seqs, lane);
     const long long run = run_length<D>(total);
     const long long begin = blockIdx.x * run, end = min(begin + run, total);
     if (begin >= end)
@@ -153,16 +162,16 @@ __global__ void __launch_bounds__(kNThreads) paged_narrow_kernel(const __grid_co
     const uint32_t a_ring = a_q + S::kQ;
 
     long long at = begin, before;
-    int seq = find_listed(p, at, lane, before);
+    int seq = find_listed<D>(p, at, lane, before);
     if (seq < 0)
         return;
-    Listed ls = list_seq(p, seq);
+    Listed ls = list_seq<D>(p, seq);
     while (at < end) {
         while (at >= before + ls.count(p)) {  // the next sequence that has entries
             before += ls.count(p);
             if (++seq >= p.pk.num_seqs)
                 return;
-            ls = list_seq(p, seq);
+            ls = list_seq<D>(p, seq);
         }
         const long long triple = (at - before) / ls.k_tiles;
         const int t0 = (int)(at - before - triple * ls.k_tiles);
@@ -178,9 +187,9 @@ __global__ void __launch_bounds__(kNThreads) paged_narrow_kernel(const __grid_co
         q.kv_end = ls.kv_end;
         int tile_hi, unused;
         visible_keys(p, q, (q.first + q.rows - 1) / p.group, unused, tile_hi);
-        const int lo = ls.lo + t0 * kNKeys;
-        const int hi = t1 == ls.k_tiles ? tile_hi : min(tile_hi, ls.lo + t1 * kNKeys);
-        const int tiles = hi > lo ? (hi - lo + kNKeys - 1) / kNKeys : 0;
+        const int lo = ls.lo + t0 * kKeys;
+        const int hi = t1 == ls.k_tiles ? tile_hi : min(tile_hi, ls.lo + t1 * kKeys);
+        const int tiles = hi > lo ? (hi - lo + kKeys - 1) / kKeys : 0;
         const int32_t* table = p.block_table + (int64_t)seq * p.table_stride;
         const uint16_t* kc = p.k_cache + (int64_t)kvh * p.head_stride;
         const uint16_t* vc = p.v_cache + (int64_t)kvh * p.head_stride;
@@ -193,14 +202,14 @@ __global__ void __launch_bounds__(kNThreads) paged_narrow_kernel(const __grid_co
             cp_async16(a_q + tile_off<D>(r, c), p.q + (int64_t)(q.row0 + token) * p.q_row_stride + head * D + c * 8, there);
         }
         auto offset_of = [&](int tile) -> int64_t {  // by thread: key tid of the tile
-            const int key = lo + tile * kNKeys + tid;
-            return tid < kNKeys && key < hi ? key_offset(p, table, key) : -1;
+            const int key = lo + tile * kKeys + tid;
+            return tid < kKeys && key < hi ? key_offset(p, table, key) : -1;
         };
         auto issue = [&](int tile) {
-            const int64_t* offs = s_offs + (tile & 1) * kNKeys;
+            const int64_t* offs = s_offs + (tile & 1) * kKeys;
             const uint32_t to = a_ring + (uint32_t)(tile % ST) * (2 * S::kTile);
 #pragma unroll
-            for (int i = 0; i < kNKeys * CH / kNThreads; ++i) {
+            for (int i = 0; i < kKeys * CH / kNThreads; ++i) {
                 const int e = tid + i * kNThreads, r = e / CH, c = e % CH;
                 const int64_t o = offs[r];
                 const bool there = o >= 0;
@@ -211,15 +220,15 @@ __global__ void __launch_bounds__(kNThreads) paged_narrow_kernel(const __grid_co
         };
 #pragma unroll 1
         for (int t = 0; t < ST - 1; ++t) {
-            if (tid < kNKeys)
-                s_offs[(t & 1) * kNKeys + tid] = offset_of(t);
+            if (tid < kKeys)
+                s_offs[(t & 1) * kKeys + tid] = offset_of(t);
             __syncthreads();
             if (t < tiles)
                 issue(t);
             cp_async_commit();  // the first group holds the queries too
         }
-        if (tid < kNKeys)
-            s_offs[((ST - 1) & 1) * kNKeys + tid] = offset_of(ST - 1);
+        if (tid < kKeys)
+            s_offs[((ST - 1) & 1) * kKeys + tid] = offset_of(ST - 1);
 
         const int g = lane >> 2;  // the thread's rows: g and g + 8
         int rlo[2], rhi[2];
@@ -256,16 +265,16 @@ __global__ void __launch_bounds__(kNThreads) paged_narrow_kernel(const __grid_co
                     ldsm4(a_q + tile_off<D>(lane & 15, 2 * ks + (lane >> 4)), qf[kKeepQ ? ks : 0]);
             }
             const uint32_t ak = a_ring + (uint32_t)(t % ST) * (2 * S::kTile), av = ak + S::kTile;
-            const int k0 = lo + t * kNKeys + warp * NK;  // the warp's first key
-            float s[2][4];
+            const int k0 = lo + t * kKeys + warp * NK;  // the warp's first key
+            float s[NK / 8][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < NK / 8; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     s[i][e] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-                uint32_t qr[4], b[4];  // keys: the warp's 16, elements 16 ks .. + 15
+                uint32_t qr[4];
                 if (kKeepQ) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -273,14 +282,18 @@ __global__ void __launch_bounds__(kNThreads) paged_narrow_kernel(const __grid_co
                 } else {
                     ldsm4(a_q + tile_off<D>(lane & 15, 2 * ks + (lane >> 4)), qr);
                 }
-                ldsm4(ak + tile_off<D>(warp * NK + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b);
-                mma16816(s[0], qr, b[0], b[1]);
-                mma16816(s[1], qr, b[2], b[3]);
+#pragma unroll
+                for (int nt = 0; nt < NK / 16; ++nt) {
+                    uint32_t b[4];  // 16 of the warp's keys, elements 16 ks .. + 15
+                    ldsm4(ak + tile_off<D>(warp * NK + nt * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b);
+                    mma16816(s[2 * nt], qr, b[0], b[1]);
+                    mma16816(s[2 * nt + 1], qr, b[2], b[3]);
+                }
             }
             const bool clear = k0 >= full_lo && k0 + NK <= full_hi && k0 + NK <= hi;
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < NK / 8; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float x = s[i][e] * p.scale_log2;
@@ -314,27 +327,30 @@ __global__ void __launch_bounds__(kNThreads) paged_narrow_kernel(const __grid_co
             }
             // nothing seen yet: exp2(-inf - 0) = 0 everywhere
             const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-            uint32_t a[4];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                float e4[4];
+            for (int nt = 0; nt < NK / 16; ++nt) {
+                uint32_t a[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    e4[e] = exp2f(s[hh][e] - base[e >> 1]);
-                    l[e >> 1] += e4[e];
+                for (int hh = 0; hh < 2; ++hh) {
+                    float e4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        e4[e] = exp2f(s[2 * nt + hh][e] - base[e >> 1]);
+                        l[e >> 1] += e4[e];
+                    }
+                    a[2 * hh] = pack2(e4[0], e4[1]);
+                    a[2 * hh + 1] = pack2(e4[2], e4[3]);
                 }
-                a[2 * hh] = pack2(e4[0], e4[1]);
-                a[2 * hh + 1] = pack2(e4[2], e4[3]);
-            }
 #pragma unroll
-            for (int dt = 0; dt < D / 16; ++dt) {
-                uint32_t b[4];  // keys: the warp's 16, elements 16 dt .. + 15
-                ldsm4_t(av + tile_off<D>(warp * NK + (lane & 15), 2 * dt + (lane >> 4)), b);
-                mma16816(o[2 * dt], a, b[0], b[1]);
-                mma16816(o[2 * dt + 1], a, b[2], b[3]);
+                for (int dt = 0; dt < D / 16; ++dt) {
+                    uint32_t b[4];  // 16 of the warp's keys, elements 16 dt .. + 15
+                    ldsm4_t(av + tile_off<D>(warp * NK + nt * 16 + (lane & 15), 2 * dt + (lane >> 4)), b);
+                    mma16816(o[2 * dt], a, b[0], b[1]);
+                    mma16816(o[2 * dt + 1], a, b[2], b[3]);
+                }
             }
-            if (tid < kNKeys)
-                s_offs[((t + ST) & 1) * kNKeys + tid] = next_off;
+            if (tid < kKeys)
+                s_offs[((t + ST) & 1) * kKeys + tid] = next_off;
         }
         cp_async_wait<0>();
         __syncthreads();  // the ring becomes the exchange buffer
@@ -412,12 +428,12 @@ __global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_con
     RowSlot s;
     if (!map_valid_row(v, p.pk.cu_seqlens, p.pk.cu_seqlens_padded, p.pk.num_seqs, p.pk.num_rows_padded, lane, s))
         return;
-    const Listed ls = list_seq(p, s.seq);
+    const Listed ls = list_seq<D>(p, s.seq);
     if (ls.n == 0)
         return;
-    const long long run = run_length<D>(listed_before(p, p.pk.num_seqs, lane));
+    const long long run = run_length<D>(listed_before<D>(p, p.pk.num_seqs, lane));
     const int row = s.local * p.group + head % p.group, r = row % kNRows;
-    const long long first = listed_before(p, s.seq, lane) +
+    const long long first = listed_before<D>(p, s.seq, lane) +
                             ((long long)(row / kNRows) * p.num_kv_heads + head / p.group) * ls.k_tiles;
     const int b0 = (int)(first / run), b1 = (int)((first + ls.k_tiles - 1) / run);
     if (b0 == b1)
@@ -468,7 +484,7 @@ cudaError_t launch_n(const PagedParams& p, cudaStream_t stream)
     using S = NShape<D>;
     cudaError_t e = cudaFuncSetAttribute(paged_narrow_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e == cudaSuccess)
-        e = launch_kernel(paged_narrow_kernel<D>, dim3(S::kBlocks), kNThreads, S::kSmem, stream, p);
+        e = launch_kernel(paged_narrow_kernel<D>, dim3(S::kBlocks), S::kThreads, S::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
     const long long warps = (long long)p.pk.num_rows_padded * p.num_q_heads;
