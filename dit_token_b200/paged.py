@@ -23,22 +23,38 @@ _ROPE_MODES = {"interleaved": 0, "half": 1, "none": 2}
 _ROPE_SCALES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 
 
-def _one_device(first: torch.Tensor, *others) -> torch.device:
+def _one_device(first: torch.Tensor, *others) -> int:
+    """The CUDA device all the tensors lie on (None stands for an absent one)."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("expected CUDA tensors")
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"all tensors must lie on one device, got {first.device} and {t.device}")
-    return first.device
+    return index
 
 
-def _on(device: torch.device, stream):
-    """The torch stream a call runs on."""
+def _stream_on(index: int, stream) -> int:
+    """The raw stream a call runs on: the device's current one, or the given."""
     if stream is None:
-        return torch.cuda.current_stream(device)
+        return torch.cuda.current_stream(index).cuda_stream if _raw_stream is None else _raw_stream(index)
     if isinstance(stream, torch.cuda.Stream):
-        if stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {device}")
-        return stream
-    return torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device_index != index:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{index}")
+        return stream.cuda_stream
+    return int(stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call_on(index: int, name: str, *args) -> None:
+    """The library launches on the current device; make it the tensors'."""
+    if torch.cuda.current_device() == index:
+        _call(name, *args)
+    else:
+        with torch.cuda.device(index):
+            _call(name, *args)
 
 
 def _ints(t: torch.Tensor, shape: tuple, what: str) -> int:
@@ -56,7 +72,11 @@ def _freqs(t: torch.Tensor, n: Optional[int], what: str) -> int:
 
 
 def _heads(t: torch.Tensor, heads: int, head_dim: int, rows: int, what: str) -> tuple:
-    ptr, stride = _rows(t, what)
+    """(pointer, row stride) of [rows, heads * head_dim] or [rows, heads, head_dim]."""
+    if t.dim() == 2 and t.dtype == torch.bfloat16 and t.is_cuda and (t.stride(1) == 1 or t.size(1) == 1):
+        ptr, stride = t.data_ptr(), t.stride(0)
+    else:
+        ptr, stride = _rows(t, what)
     if t.size(0) != rows or t.numel() != rows * heads * head_dim:
         raise ValueError(f"{what}: expected {rows} rows of {heads} heads of {head_dim}, got {tuple(t.shape)}")
     # one row has no stride of its own: torch may report any
@@ -65,26 +85,29 @@ def _heads(t: torch.Tensor, heads: int, head_dim: int, rows: int, what: str) -> 
 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, heads: int, head_dim: int,
            B: int) -> tuple:
-    for t, what in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != torch.bfloat16 or not t.is_cuda:
-            raise TypeError(f"{what}: expected a bfloat16 CUDA tensor")
-        if t.dim() != 4 or t.size(2) != heads or t.size(3) != head_dim or t.stride(3) != 1:
-            raise ValueError(f"{what}: expected [pages, page_size, {heads}, {head_dim}] with a contiguous last axis")
-    if k_cache.shape != v_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    pages, page_size = k_cache.size(0), k_cache.size(1)
+    shape = k_cache.shape
+    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16 or not (k_cache.is_cuda and v_cache.is_cuda):
+        raise TypeError("k_cache, v_cache: expected bfloat16 CUDA tensors")
+    if len(shape) != 4 or shape[2] != heads or shape[3] != head_dim or v_cache.shape != shape:
+        raise ValueError(f"k_cache, v_cache: expected [pages, page_size, {heads}, {head_dim}], got {tuple(shape)} and "
+                         f"{tuple(v_cache.shape)}")
+    pages, page_size = shape[0], shape[1]
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("k_cache, v_cache: the last axis must be contiguous")
 
-    def strides(t):  # an axis of one entry has no stride: any multiple of 8 does
-        return (t.stride(0) if pages > 1 else page_size * heads * head_dim,
-                t.stride(1) if page_size > 1 else max(head_dim, t.stride(1) // 8 * 8),
-                t.stride(2) if heads > 1 else head_dim)
-    if strides(k_cache) != strides(v_cache):
+    def strides(st):  # an axis of one entry has no stride: any multiple of 8 does
+        return (st[0] if pages > 1 else page_size * heads * head_dim,
+                st[1] if page_size > 1 else max(head_dim, st[1] // 8 * 8),
+                st[2] if heads > 1 else head_dim)
+    ks = strides(ks)
+    if ks != strides(vs):
         raise ValueError("k_cache and v_cache must have the same strides")
     if block_table.dtype != torch.int32 or not block_table.is_cuda or block_table.dim() != 2 or \
             block_table.size(0) != B or (block_table.size(1) > 1 and block_table.stride(1) != 1):
         raise TypeError("block_table: expected an int32 CUDA tensor [num_seqs, max_pages], contiguous rows")
     table_stride = block_table.stride(0) if B > 1 else block_table.size(1)
-    return (k_cache.data_ptr() or None, v_cache.data_ptr() or None, *strides(k_cache), pages, page_size), \
+    return (k_cache.data_ptr() or None, v_cache.data_ptr() or None, *ks, pages, page_size), \
         (block_table.data_ptr() or None, table_stride, block_table.size(1))
 
 
@@ -158,10 +181,8 @@ def dit_qk_rope_scaled(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tenso
     wq, wk = _weights(q_weight, k_weight, head_dim)
     fp, rotary, gp, gf, st, sh, sw, po, gain, eps, mode = _rope_args(
         freqs, rope_grid, grid_freqs, sections, pos_offset, attn_scale, eps, rope_mode, B)
-    with torch.cuda.device(dev):
-        _call("dit_qk_rope_scaled", qp, qs, kp, ks, qop, qos, kop, kos, wq, wk, cs, cp, B, rows, num_q_heads,
-              num_k_heads, head_dim, fp, rotary, gp, gf, st, sh, sw, po, gain, eps, mode,
-              _on(dev, stream).cuda_stream)
+    _call_on(dev, "dit_qk_rope_scaled", qp, qs, kp, ks, qop, qos, kop, kos, wq, wk, cs, cp, B, rows, num_q_heads,
+             num_k_heads, head_dim, fp, rotary, gp, gf, st, sh, sw, po, gain, eps, mode, _stream_on(dev, stream))
     return qo, ko
 
 
@@ -194,10 +215,9 @@ def dit_qkv_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cac
     cache, table = _cache(k_cache, v_cache, block_table, num_kv_heads, head_dim, B)
     fp, rotary, gp, gf, st, sh, sw, po, gain, eps, mode = _rope_args(
         freqs, rope_grid, grid_freqs, sections, pos_offset, attn_scale, eps, rope_mode, B)
-    with torch.cuda.device(dev):
-        _call("dit_qkv_rope_append", qp, qs, kp, ks, vp, vs, qop, qos, wq, wk, *cache, *table,
-              _ints(cache_lens, (B,), "cache_lens"), cs, cp, B, rows, num_q_heads, num_kv_heads, head_dim, fp, rotary,
-              gp, gf, st, sh, sw, po, gain, eps, mode, _on(dev, stream).cuda_stream)
+    _call_on(dev, "dit_qkv_rope_append", qp, qs, kp, ks, vp, vs, qop, qos, wq, wk, *cache, *table,
+             _ints(cache_lens, (B,), "cache_lens"), cs, cp, B, rows, num_q_heads, num_kv_heads, head_dim, fp, rotary,
+             gp, gf, st, sh, sw, po, gain, eps, mode, _stream_on(dev, stream))
     return qo
 
 
@@ -241,21 +261,21 @@ def dit_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise TypeError("workspace: expected a contiguous uint8 CUDA tensor")
     scale = 1.0 / math.sqrt(head_dim) if softmax_scale is None else float(softmax_scale)
-    on = _on(dev, stream)
-    # what is allocated here belongs to the stream that uses it
-    with torch.cuda.device(dev), torch.cuda.stream(on):
-        if out is None:
-            out = torch.empty((rows, num_q_heads * head_dim), dtype=q.dtype, device=dev)
-        op, os_ = _heads(out, num_q_heads, head_dim, rows, "out")
-        if workspace is None and rows > 0 and B > 0:
-            capacity = max(1, min(table[2] * cache[6], 2**31 - 1))
-            nbytes = dit_paged_attention_workspace(
-                rows, B, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, head_dim=head_dim, max_chunk=max_chunk,
-                max_kv_len=min(max_kv_len, capacity) if max_kv_len > 0 else capacity)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        nbytes = 0 if workspace is None else workspace.numel()
-        _call("dit_paged_attention", qp, qs, *cache, *table, lens, cs, cp, B, rows, num_q_heads, num_kv_heads,
-              head_dim, scale, int(bool(causal)), int(window), int(max_chunk), int(max_kv_len), op, os_,
-              None if lse is None else lse.data_ptr(), workspace.data_ptr() or None if nbytes else None, nbytes,
-              on.cuda_stream)
+    on = _stream_on(dev, stream)
+    if out is None or (workspace is None and rows > 0 and B > 0):
+        # what is allocated here belongs to the stream that uses it
+        with torch.cuda.device(dev), torch.cuda.stream(torch.cuda.ExternalStream(on, device=dev)):
+            if out is None:
+                out = torch.empty((rows, num_q_heads * head_dim), dtype=q.dtype, device=q.device)
+            if workspace is None:
+                capacity = max(1, min(table[2] * cache[6], 2**31 - 1))
+                workspace = torch.empty(dit_paged_attention_workspace(
+                    rows, B, num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, head_dim=head_dim,
+                    max_chunk=max_chunk, max_kv_len=min(max_kv_len, capacity) if max_kv_len > 0 else capacity),
+                    dtype=torch.uint8, device=q.device)
+    op, os_ = _heads(out, num_q_heads, head_dim, rows, "out")
+    nbytes = 0 if workspace is None else workspace.numel()
+    _call_on(dev, "dit_paged_attention", qp, qs, *cache, *table, lens, cs, cp, B, rows, num_q_heads, num_kv_heads,
+             head_dim, scale, int(bool(causal)), int(window), int(max_chunk), int(max_kv_len), op, os_,
+             None if lse is None else lse.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes, on)
     return out
