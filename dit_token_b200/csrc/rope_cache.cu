@@ -74,6 +74,84 @@ __device__ __forceinline__ void store_quads(uint16_t* head, int o0, int o1, uint
         st_stream(head + o0, v);
 }
 
+// What a pair's elements are multiplied by: with weights these are folded into
+// the rotation, (o_a, o_b) = r (x_a c0 + x_b c1, x_a c2 + x_b c3), so that a
+// normed and turned pair costs two products, two fused ones and r.  A lane that
+// passes has c0 = w_a, c3 = w_b and zeros.  One set is kept, and folded again
+// between q's heads and k's: kept for both, registers (126 against 96 a thread)
+// leave fewer warps resident, 197 us for the long video against 171; without
+// weights (150 us, 104 % of the measured copy rate) there is one set anyway.
+struct PairCoef {
+    float c0[4], c1[4], c2[4], c3[4];
+};
+
+template <int MODE>
+__device__ __forceinline__ void pair_regs(int e, int& a, int& z)
+{
+    a = MODE == kRopeHalf ? e : 2 * e;
+    z = MODE == kRopeHalf ? 4 + e : 2 * e + 1;
+}
+
+template <int MODE, bool NORM>
+__device__ __forceinline__ void fold(PairCoef& pc, const float (&c)[4], const float (&s)[4], const uint16_t* w, int o0,
+                                     int o1)
+{
+    float wf[8];
+    if (NORM) {
+        const uint2 wa = __ldg(reinterpret_cast<const uint2*>(w + o0));
+        const uint2 wb = __ldg(reinterpret_cast<const uint2*>(w + o1));
+        unpack8(make_uint4(wa.x, wa.y, wb.x, wb.y), wf);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        int a, z;
+        pair_regs<MODE>(e, a, z);
+        const float wa = NORM ? wf[a] : 1.f, wz = NORM ? wf[z] : 1.f;
+        pc.c0[e] = wa * c[e];
+        pc.c1[e] = -wz * s[e];
+        pc.c2[e] = wa * s[e];
+        pc.c3[e] = wz * c[e];
+    }
+}
+
+template <int D, int MODE, bool NORM, int U>
+__device__ __forceinline__ void turn_batch(uint16_t* to, int64_t step, int heads, int h0, int o0, int o1, bool keep,
+                                           bool turns, float eps, const PairCoef& pc, const uint4 (&x)[U])
+{
+    constexpr int LPH = D / 8, HPW = kWarp / LPH;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * HPW;
+        float r = 1.f;
+        if (NORM) {
+            const uint32_t wd[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            f32x2 ss2 = f2_make(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f32x2 xx = f2_from_bf16x2(wd[e]);
+                ss2 = f2_fma(xx, xx, ss2);
+            }
+            const float ss = group_sum<LPH>(ss2.x + ss2.y);  // every lane of the warp takes part
+            r = rsqrtf(ss * (1.0f / (float)D) + eps);
+        }
+        float v[8], o[8];
+        unpack8(x[u], v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            int a, z;
+            pair_regs<MODE>(e, a, z);
+            const float oa = fmaf(v[z], pc.c1[e], v[a] * pc.c0[e]), oz = fmaf(v[z], pc.c3[e], v[a] * pc.c2[e]);
+            o[a] = NORM ? r * oa : oa;
+            o[z] = NORM ? r * oz : oz;
+        }
+        uint4 out = pack8(o);
+        if (!NORM && !turns)
+            out = x[u];  // passes bit for bit
+        if (h < heads && to != nullptr)
+            store_quads<MODE>(to + (int64_t)h * step, o0, o1, out, keep);
+    }
+}
+
 template <int D, int MODE, bool NORM, int U>
 __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __grid_constant__ RopeCacheParams p)
 {
@@ -138,7 +216,7 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
     load(b0, cur);
 
     // cos and sin (times g) of the lane's four pairs
-    float c[4], sn[4];
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
     if (turns && b0 < nq + nk) {
         const int off = p.pos_offset != nullptr ? max(__ldg(p.pos_offset + s.seq), 0) : before;
         const RowPosition rp = row_position((long long)s.local + off,
@@ -156,56 +234,27 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
             sn[e] *= p.attn_scale;
         }
     }
+    PairCoef pc;
+    fold<MODE, NORM>(pc, c, sn, b0 < nq ? p.q_weight : p.k_weight, o0, o1);
 
+    const bool cached = p.block_table != nullptr;
     for (int b = b0; b < b1; ++b) {
         uint4 nxt[U];
         if (b + 1 < b1)
             load(b + 1, nxt);
-        const bool is_q = b < nq, is_v = b >= nq + nk;
-        uint16_t* to = is_q ? q_to : (is_v ? v_to : k_to);
-        const int64_t step = is_q ? D : head_step;
-        const int heads = is_q ? p.num_q_heads : p.num_k_heads;
-        const int h0 = (is_q ? b : (is_v ? b - nq - nk : b - nq)) * HB + sub;
-        const bool keep = !is_q && p.block_table != nullptr;
-        float w[8];
-        if (NORM && !is_v) {
-            const uint16_t* wp = is_q ? p.q_weight : p.k_weight;
-            const uint2 wa = __ldg(reinterpret_cast<const uint2*>(wp + o0));
-            const uint2 wb = __ldg(reinterpret_cast<const uint2*>(wp + o1));
-            unpack8(make_uint4(wa.x, wa.y, wb.x, wb.y), w);
-        }
+        if (NORM && b == nq && b > b0)  // from q's heads to k's
+            fold<MODE, NORM>(pc, c, sn, p.k_weight, o0, o1);
+        if (b < nq + nk) {
+            const bool is_q = b < nq;
+            turn_batch<D, MODE, NORM, U>(is_q ? q_to : k_to, is_q ? D : head_step, is_q ? p.num_q_heads : p.num_k_heads,
+                                         (is_q ? b : b - nq) * HB + sub, o0, o1, !is_q && cached, turns, p.eps, pc, cur);
+        } else if (v_to != nullptr) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + u * HPW;
-            uint4 out = cur[u];
-            if (!is_v) {
-                float x[8], o[8];
-                unpack8(cur[u], x);
-                if (NORM) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        ss = fmaf(x[e], x[e], ss);
-                    ss = group_sum<LPH>(ss);  // every lane of the warp takes part
-                    const float r = rsqrtf(ss * (1.0f / (float)D) + p.eps);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] *= r * w[e];
-                }
-                if (turns) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int a = MODE == kRopeHalf ? e : 2 * e, z = MODE == kRopeHalf ? 4 + e : 2 * e + 1;
-                        o[a] = fmaf(x[a], c[e], -x[z] * sn[e]);
-                        o[z] = fmaf(x[a], sn[e], x[z] * c[e]);
-                    }
-                    out = pack8(o);
-                } else if (NORM) {
-                    out = pack8(x);
-                }  // else the element passes bit for bit
+            for (int u = 0; u < U; ++u) {
+                const int h = (b - nq - nk) * HB + sub + u * HPW;
+                if (h < p.num_k_heads)
+                    store_quads<MODE>(v_to + (int64_t)h * head_step, o0, o1, cur[u], true);
             }
-            if (h < heads && to != nullptr)
-                store_quads<MODE>(to + (int64_t)h * step, o0, o1, out, keep);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -239,7 +288,7 @@ cudaError_t launch_rc(RopeCacheParams p, int mode, cudaStream_t stream)
 cudaError_t launch_rope_cache(const RopeCacheParams& p, int head_dim, int rope_mode, cudaStream_t stream)
 {
     switch (head_dim) {
-    case 64: return launch_rc<64, 2>(p, rope_mode, stream);
+    case 64: return launch_rc<64, 4>(p, rope_mode, stream);
     case 128: return launch_rc<128, 4>(p, rope_mode, stream);
     case 256: return launch_rc<256, 4>(p, rope_mode, stream);
     default: return cudaErrorInvalidValue;
