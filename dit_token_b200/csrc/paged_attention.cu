@@ -12,9 +12,8 @@
 // The rows of a tile are the (token, head) pairs that share a key head, so
 // grouped heads read each key once.  A block takes 64 of them, 16 per warp,
 // and every warp all keys of a tile.  This is the kernel of the chunks that the
-// tensor-memory kernel does not take (heads of 256; caches whose strides or
-// page size TMA cannot follow); paged_attention_narrow.cu is that of next
-// tokens.
+// tensor-memory kernel does not take (caches whose strides or page size TMA
+// cannot follow); paged_attention_narrow.cu is that of next tokens.
 // Key and value tiles arrive by 16-byte asynchronous copies, which take any
 // page size and stride and write zeros for keys that are not there; STAGES
 // tiles are in flight.
@@ -391,8 +390,8 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
         plan.bytes = plan.most_bytes = plan.part_rows * (head_dim * 4 + 8);
         return true;
     }
-    plan.kind = head_dim == 256 || !regular ? kPagedWide : kPagedTc;
-    plan.tile_rows = plan.kind == kPagedWide ? 64 : 256;
+    plan.kind = regular ? kPagedTc : kPagedWide;
+    plan.tile_rows = plan.kind == kPagedWide ? 64 : (head_dim == 256 ? 128 : 256);
     // ceil over each sequence adds at most one tile per sequence
     const int64_t tiles = rows * group / plan.tile_rows + (num_seqs < rows ? num_seqs : rows);
     if (tiles > INT32_MAX)
@@ -412,7 +411,7 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
         // each costs its block's start and end (about 9 us, four steps) and the
         // write and read of its part (a chunk of 1,000 rows of 40 heads over
         // itself: 59 us whole, 185 in 4 splits), so runs are 512 keys at least.
-        splits = 148 / blocks;
+        splits = 160 / blocks;
         const int64_t most = keys / 512;
         splits = splits < most ? splits : most;
     } else {

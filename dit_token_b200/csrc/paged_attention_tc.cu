@@ -1,6 +1,6 @@
 // paged_attention_tc.cu -- attention of a chunk of new tokens over a paged
 // cache on the fifth-generation tensor cores (tcgen05, accumulators in tensor
-// memory), for heads of 64 and 128.
+// memory).
 //
 // The mathematics is paged_attention.cu's: one pass over the keys with the
 // running maximum m, sum l and unnormalised o of a softmax, in fp32, the
@@ -28,7 +28,7 @@
 // Steps begin at multiples of 128 keys, so boxes keep their alignment.
 // The two tiles alternate: while one's softmax runs, the other's products do.
 // Tensor memory (512 columns of 128 lanes x 32 bits): s0, s1 (128 each), o0,
-// o1 (D each); p takes the second half of its s, once the row is in registers.
+// o1 (D each; heads of 256 leave room for one tile per block); p takes the second half of its s, once the row is in registers.
 // The products of one tile are issued in the order o(i), s(i+1), and a
 // commit covers everything issued before it, so "s(i+1) is there" also says
 // that o(i) is complete and p(i) is free.
@@ -45,17 +45,17 @@ namespace {
 constexpr int kTcRows = 128;   // rows per tile
 constexpr int kTcKeys = 128;   // keys per step
 constexpr int kTcThreads = 384;
-constexpr int kTcSoftmaxThreads = 256;
 constexpr uint32_t kBlockBytes = kTcKeys * 128;  // 128 rows of 64 elements
 constexpr float kTcLag = 8.f;  // log2 of how far probabilities may pass 1
 constexpr long long kWaitCycles = 4000000000ll;  // a wait gives up after about two seconds
 
 template <int D>
 struct TcShape {
-    static constexpr int kSlots = D == 128 ? 4 : 8;              // key or value tiles in shared memory
+    static constexpr int kTiles = D == 256 ? 1 : 2;              // query tiles of a block
+    static constexpr int kSlots = D == 256 ? 2 : (D == 128 ? 4 : 8);  // key or value tiles in shared memory
     static constexpr uint32_t kTile = (D / 64) * kBlockBytes;    // bytes of a tile (q, k or v)
-    static constexpr uint32_t kQ = 0;                            // two query tiles
-    static constexpr uint32_t kRing = 2 * kTile;
+    static constexpr uint32_t kQ = 0;
+    static constexpr uint32_t kRing = kTiles * kTile;
     static constexpr uint32_t kBars = kRing + kSlots * kTile;
     static constexpr int kNumBars = 2 * kSlots + 11;
     static constexpr uint32_t kTmemPtr = kBars + kNumBars * 8;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     const int kvh = blockIdx.y, split = blockIdx.z;
     QueryTile q;
     // later tiles of a causal chunk see more keys: they go first
-    if (!map_query_tile((int)(gridDim.x - 1 - blockIdx.x), p, 2 * kTcRows, lane, q))
+    if (!map_query_tile((int)(gridDim.x - 1 - blockIdx.x), p, S::kTiles * kTcRows, lane, q))
         return;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kAbort);
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
         }
-        mbar_init(q_full, kTcSoftmaxThreads);
+        mbar_init(q_full, S::kTiles * kTcRows);
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
             mbar_init(p_full(t, 0), 4);
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         const bool mine = r < have;
         const int at = q.first + t * kTcRows + min(r, max(have - 1, 0));
         const int token = at / p.group, head = kvh * p.group + at % p.group;
-        if (steps > 0) {
+        if (steps > 0 && t < S::kTiles) {
             // a warp copies the queries of its own 32 rows, RPI rows at a time
             constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte chunks per row, rows per instruction
             const int64_t mine_at = (int64_t)(q.row0 + token) * p.q_row_stride + head * D;
@@ -720,7 +720,12 @@ bool cache_rows(int64_t page_stride, int64_t slot_stride, int64_t head_stride, i
 
 cudaError_t launch_paged_attention_tc(const PagedParams& p, int tiles, int head_dim, cudaStream_t stream)
 {
-    return head_dim == 128 ? launch_tc<128>(p, tiles, stream) : launch_tc<64>(p, tiles, stream);
+    switch (head_dim) {
+    case 64: return launch_tc<64>(p, tiles, stream);
+    case 128: return launch_tc<128>(p, tiles, stream);
+    case 256: return launch_tc<256>(p, tiles, stream);
+    default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace dit
