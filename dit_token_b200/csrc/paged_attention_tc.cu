@@ -49,11 +49,16 @@ constexpr uint32_t kBlockBytes = kTcKeys * 128;  // 128 rows of 64 elements
 constexpr float kTcLag = 8.f;  // log2 of how far probabilities may pass 1
 constexpr long long kWaitCycles = 4000000000ll;  // a wait gives up after about two seconds
 
-template <int D>
+// WHOLE: boxes of 8 rows of whole heads, else of 64 elements.  (A template:
+// with strides read at run time the issuing warp fell behind, 2355 -> 2473 us
+// for the video chunk.)
+template <int D, bool WHOLE>
 struct TcShape {
     static constexpr int kTiles = D == 256 ? 1 : 2;              // query tiles of a block
     static constexpr int kSlots = D == 256 ? 2 : (D == 128 ? 4 : 8);  // key or value tiles in shared memory
     static constexpr uint32_t kTile = (D / 64) * kBlockBytes;    // bytes of a tile (q, k or v)
+    static constexpr uint32_t kGroup = WHOLE ? 1024 * (D / 64) : 1024;   // between a tile's 8-row groups
+    static constexpr uint32_t kBlock = WHOLE ? 1024 : kBlockBytes;       // and its 64-element blocks
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = kTiles * kTile;
     static constexpr uint32_t kBars = kRing + kSlots * kTile;
@@ -108,6 +113,12 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
                  "[%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+// The same over whole heads: column block z on.
+__device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* map, int y, int z, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 // This thread's writes to shared memory, visible to the tensor cores' proxy.
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -180,12 +191,12 @@ __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sy
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptor, rows of 128 bytes permuted in 16-byte chunks
-// by the row's low 3 bits (128-byte swizzle), 8-row groups 1024 bytes apart.
-// `lead` (16-byte units) is the distance of 64-element blocks along the
-// contiguous axis, read only where that axis is the product's outer one (v).
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead)
+// by the row's low 3 bits (128-byte swizzle), 8-row groups `group` bytes apart.
+// `lead` is the distance of 64-element blocks along the contiguous axis, read
+// only where that axis is the product's outer one (v).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t group, uint32_t lead)
 {
-    return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)lead << 16) | ((uint64_t)(1024 >> 4) << 32) |
+    return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(group >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
 // Instruction descriptor: bf16 operands, fp32 accumulator, M x N, b along its
@@ -260,11 +271,11 @@ __device__ __forceinline__ uint32_t tc_off(int r, int c)
     return (uint32_t)(c >> 3) * kBlockBytes + (uint32_t)(r * 128 + (((c ^ r) & 7) << 4));
 }
 
-template <int D>
+template <int D, bool WHOLE>
 __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap k_map,
                           const __grid_constant__ CUtensorMap v_map)
 {
-    using S = TcShape<D>;
+    using S = TcShape<D, WHOLE>;
     constexpr int NS = S::kSlots;
     extern __shared__ __align__(1024) unsigned char smem[];
     grid_dependency_wait();
@@ -355,7 +366,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             // The whole warp walks the steps and one lane issues: operands
             // that every lane shares stay in uniform registers.  (With one
             // lane alone in the loop each product's operands were moved there
-            // first, some 100 cycles per product of 64: MMAFIG.)
+            // first, some 100 cycles per product of 64: the video chunk's
+            // products alone 2036 us against 1781.)
             constexpr uint32_t kIdescS = TcIdesc<kTcRows, kTcKeys, false>::value;
             constexpr uint32_t kIdescO = TcIdesc<kTcRows, D, true>::value;
             auto in = [&](int t, int i) { return i >= first[t] && i < last[t]; };
@@ -364,8 +376,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = (uint32_t)(ks >> 2) * kBlockBytes + (uint32_t)(ks & 3) * 32;
-                        tc_mma_ss(t * kTcKeys, smem_desc(a + off, 1), smem_desc(b + off, 1), kIdescS, ks > 0);
+                        const uint32_t c = ks >> 2, in = (ks & 3) * 32;
+                        tc_mma_ss(t * kTcKeys, smem_desc(a + c * kBlockBytes + in, 1024, 16),
+                                  smem_desc(b + c * S::kBlock + in, S::kGroup, 16), kIdescS, ks > 0);
                     }
                     tc_commit(s_full(t));
                 }
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = h * (kTcKeys / 32); ks < (h + 1) * (kTcKeys / 32); ++ks)
-                        tc_mma_ts(2 * kTcKeys + t * D, t * kTcKeys + kTcKeys / 2 + ks * 8, smem_desc(b + ks * 2048, kBlockBytes >> 4),
+                        tc_mma_ts(2 * kTcKeys + t * D, t * kTcKeys + kTcKeys / 2 + ks * 8, smem_desc(b + ks * 2 * S::kGroup, S::kGroup, S::kBlock),
                                   kIdescO, add || ks > 0);
                 }
                 __syncwarp();
@@ -469,10 +482,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                     mbar_expect(full(slot), boxes * (uint32_t)box * (D * 2));
                 __syncwarp();
                 if (there) {
-                    const uint32_t to = base + S::kRing + slot * S::kTile + (uint32_t)(lane * box) * 128;
+                    const uint32_t to = base + S::kRing + slot * S::kTile + (uint32_t)(lane * (box / 8)) * S::kGroup;
+                    const CUtensorMap* map = (j & 1) ? &v_map : &k_map;
+                    if (WHOLE) {
+                        tma_box3(to, map, row, x / 64, full(slot));
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_box(to + c * kBlockBytes, (j & 1) ? &v_map : &k_map, x + 64 * c, row, full(slot));
+                        for (int c = 0; c < D / 64; ++c)
+                            tma_box(to + c * kBlockBytes, map, x + 64 * c, row, full(slot));
+                    }
                 }
                 __syncwarp();
             }
@@ -482,9 +500,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 const int slot = (j - 1) % NS;
                 if (__all_sync(0xffffffffu, mbar_wait(full(slot), (uint32_t)((j - 1) / NS) & 1u, abort))) {
                     for (int c = 0; c < D / 64; ++c)
-                        for (int e = behind * 8 + lane; e < kTcKeys * 8; e += 32)
-                            *reinterpret_cast<uint4*>(smem + S::kRing + slot * S::kTile + c * kBlockBytes + e * 16) =
+                        for (int e = behind * 8 + lane; e < kTcKeys * 8; e += 32) {
+                            const int r = e >> 3;
+                            *reinterpret_cast<uint4*>(smem + S::kRing + slot * S::kTile + c * S::kBlock +
+                                                      (r >> 3) * S::kGroup + (r & 7) * 128 + (e & 7) * 16) =
                                 make_uint4(0u, 0u, 0u, 0u);
+                        }
                     proxy_fence();
                     __syncwarp();
                     if (lane == 0)
@@ -647,7 +668,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
 // The cache as rows of one head's elements, slot_stride apart: element x of row
 // g * page_rows + s (+ head_rows per head) is what the caller calls page g,
 // slot s, with a head's columns from h * head_cols.
-bool cache_map(CUtensorMap& map, const PagedParams& p, const uint16_t* cache, int head_dim, int64_t rows, int64_t cols)
+bool cache_map(CUtensorMap& map, const PagedParams& p, const uint16_t* cache, int head_dim, bool whole,
+               const CacheRows& c)
 {
     using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -660,33 +682,46 @@ bool cache_map(CUtensorMap& map, const PagedParams& p, const uint16_t* cache, in
             fn = nullptr;
         return reinterpret_cast<Encode>(fn);
     }();
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)p.slot_stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)p.box_rows}, step[2] = {1, 1};
+    const cuuint64_t heads[3] = {64, (cuuint64_t)c.rows, (cuuint64_t)c.cols / 64};
+    const cuuint64_t flat[2] = {(cuuint64_t)c.cols, (cuuint64_t)c.rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.slot_stride * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.box_rows, (cuuint32_t)head_dim / 64}, step[3] = {1, 1, 1};
     return encode != nullptr &&
-           encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(cache), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, whole ? 3 : 2, const_cast<uint16_t*>(cache),
+                  whole ? heads : flat, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-cudaError_t launch_tc(PagedParams p, int tiles, cudaStream_t stream)
+template <int D, bool WHOLE>
+cudaError_t launch_tc_boxes(PagedParams p, const CacheRows& c, int tiles, cudaStream_t stream)
 {
-    CacheRows c;
     CUtensorMap k_map, v_map;
-    if (!cache_rows(p.page_stride, p.slot_stride, p.head_stride, p.num_pages, p.page_size, p.num_kv_heads, D, c))
-        return cudaErrorInvalidValue;
     p.page_rows = c.page_rows;
     p.head_rows = c.head_rows;
     p.head_cols = c.head_cols;
-    p.box_rows = c.box_rows;
-    if (!cache_map(k_map, p, p.k_cache, D, c.rows, c.cols) || !cache_map(v_map, p, p.v_cache, D, c.rows, c.cols))
+    p.box_rows = WHOLE ? 8 : c.box_rows;
+    if (!cache_map(k_map, p, p.k_cache, D, WHOLE, c) || !cache_map(v_map, p, p.v_cache, D, WHOLE, c))
         return cudaErrorInvalidValue;
-    auto* kernel = paged_attention_tc_kernel<D>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D>::kSmem);
+    auto* kernel = paged_attention_tc_kernel<D, WHOLE>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, TcShape<D, WHOLE>::kSmem);
     if (e != cudaSuccess)
         return e;
     return launch_kernel(kernel, dim3((unsigned)tiles, (unsigned)p.num_kv_heads, (unsigned)p.splits), kTcThreads,
-                         TcShape<D>::kSmem, stream, p, k_map, v_map);
+                         TcShape<D, WHOLE>::kSmem, stream, p, k_map, v_map);
+}
+
+template <int D>
+cudaError_t launch_tc(const PagedParams& p, int tiles, cudaStream_t stream)
+{
+    CacheRows c;
+    if (!cache_rows(p.page_stride, p.slot_stride, p.head_stride, p.num_pages, p.page_size, p.num_kv_heads, D, c))
+        return cudaErrorInvalidValue;
+    // whole heads where they make fewer boxes of a tile
+    if constexpr (D > 64)
+        if (kTcKeys / c.box_rows * (D / 64) > kTcKeys / 8 && c.head_cols % 64 == 0)
+            return launch_tc_boxes<D, true>(p, c, tiles, stream);
+    return launch_tc_boxes<D, false>(p, c, tiles, stream);
 }
 
 }  // namespace
