@@ -651,6 +651,8 @@ dit_status dit_paged_attention(const void* q, int64_t q_row_stride, const void* 
         !aligned4(lse))
         return DIT_ERR_ALIGN;
     const int64_t capacity = (int64_t)max_pages * page_size;
+    if (capacity > INT32_MAX - 4096)  // key numbers, a tile beyond the last, are 32-bit
+        return DIT_ERR_UNSUPPORTED;
     int64_t keys = max_kv_len > 0 && max_kv_len < capacity ? max_kv_len : capacity;
     keys = keys < 1 ? 1 : (keys > INT32_MAX ? INT32_MAX : keys);
     dit::PagedPlan plan{};

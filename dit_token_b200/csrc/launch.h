@@ -197,6 +197,10 @@ struct PagedParams {
     float scale_log2;               // softmax scale times log2(e)
     int32_t causal, window;         // window 0: none
     int32_t splits, split_keys;
+    // Which sequences a launch takes, by their rows (tokens times group): a
+    // mixed batch's few-row ones go to the narrow kernel (narrow_rows at most),
+    // the others (more than skip_rows) to the one for chunks.
+    int32_t narrow_rows, skip_rows;
     int32_t page_rows, head_rows, head_cols, box_rows;  // see CacheRows; set by the launcher that uses them
 };
 
@@ -215,13 +219,15 @@ bool cache_rows(int64_t page_stride, int64_t slot_stride, int64_t head_stride, i
 constexpr int kPagedNarrow = 0;
 constexpr int kPagedWide = 1;
 constexpr int kPagedTc = 2;
+constexpr int kNarrowRows = 32;  // rows (tokens times group) the narrow kernel is for: two tiles
 struct PagedPlan {
     int kind;
+    bool mixed;      // the narrow kernel runs before the other, for the few-row sequences
     int tile_rows;
     int tiles;       // upper bound of the batch's query tiles
     int splits;
     int split_keys;
-    int64_t part_rows;   // rows of partial sums in the workspace
+    int64_t part_rows;   // rows of partial sums in the workspace, the narrow kernel's first
     int64_t bytes;       // workspace of this call
     int64_t most_bytes;  // of any window and shorter key axis at these sizes
 };
@@ -231,7 +237,8 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
                 int64_t max_kv_len, int64_t window, bool regular, PagedPlan& plan);
 cudaError_t launch_paged_attention_tc(const PagedParams& p, int tiles, int head_dim, cudaStream_t stream);
 int64_t paged_narrow_slots(int head_dim);  // rows of partial sums it wants
-cudaError_t launch_paged_attention_narrow(const PagedParams& p, int head_dim, cudaStream_t stream);
+// mixed: narrow_rows leaves the batch's other sequences out
+cudaError_t launch_paged_attention_narrow(const PagedParams& p, bool mixed, int head_dim, cudaStream_t stream);
 cudaError_t launch_paged_attention(const PagedParams& p, const PagedPlan& plan, int head_dim, cudaStream_t stream);
 
 cudaError_t launch_rope_cache(const RopeCacheParams& p, int head_dim, int rope_mode, cudaStream_t stream);

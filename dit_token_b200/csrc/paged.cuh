@@ -40,7 +40,7 @@ __device__ __forceinline__ bool map_query_tile(int t, const PagedParams& p, int 
             if (row0 < 0 || c0 < 0 || n <= 0 || (long long)row0 + n > p.pk.num_rows_padded ||
                 (long long)c0 + n > p.pk.num_rows_padded)
                 n = 0;
-            tiles = (int)(((long long)n * p.group + R - 1) / R);
+            tiles = (long long)n * p.group <= p.skip_rows ? 0 : (int)(((long long)n * p.group + R - 1) / R);
         }
         int sum = tiles;
 #pragma unroll

@@ -309,6 +309,8 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     RowSlot s;
     if (!map_valid_row(v, p.pk.cu_seqlens, p.pk.cu_seqlens_padded, p.pk.num_seqs, p.pk.num_rows_padded, lane, s))
         return;
+    if ((long long)(__ldg(p.pk.cu_seqlens + s.seq + 1) - __ldg(p.pk.cu_seqlens + s.seq)) * p.group <= p.skip_rows)
+        return;  // the narrow kernel's
     const int64_t part = partial_index(p, v, head, 0);
     float mm = -INFINITY;
     for (int i = lane; i < p.splits; i += 32)
@@ -383,13 +385,20 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
     const int64_t group = num_q_heads / num_kv_heads;
     const int64_t chunk = max_chunk > 0 && max_chunk < rows ? max_chunk : rows;
     plan = PagedPlan{};
-    if (chunk * group <= 32) {
+    const int64_t narrow = paged_narrow_slots(head_dim);
+    if (chunk * group <= kNarrowRows) {
         plan.kind = kPagedNarrow;
         plan.splits = 1;
-        plan.part_rows = paged_narrow_slots(head_dim);
-        plan.bytes = plan.most_bytes = plan.part_rows * (head_dim * 4 + 8);
+        plan.part_rows = narrow;
+        plan.bytes = plan.most_bytes = narrow * (head_dim * 4 + 8);
         return true;
     }
+    // Next tokens beside chunks would each take a whole block per key head of
+    // the chunk kernel, one row of 256: they go to the narrow kernel first (a
+    // chunk of 2,000 rows and 31 next tokens over 3,000 to 27,000 keys: 664 us
+    // -> 532).  Where a batch turns out to hold none its launches cost 5 us, so
+    // not where the rows given leave no sequence that short.
+    plan.mixed = num_seqs > 1 && rows <= (num_seqs - 1) * chunk + kNarrowRows;
     plan.kind = regular ? kPagedTc : kPagedWide;
     plan.tile_rows = plan.kind == kPagedWide ? 64 : (head_dim == 256 ? 128 : 256);
     // ceil over each sequence adds at most one tile per sequence
@@ -425,7 +434,8 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
         splits = 1;
     // splits only falls below its value here, and that grows with the keys:
     // what one workspace must hold for every window and shorter length
-    plan.most_bytes = splits == 1 ? 0 : part * splits;
+    const int64_t narrow_part = plan.mixed ? narrow * (head_dim * 4 + 8) : 0;
+    plan.most_bytes = narrow_part + (splits == 1 ? 0 : part * splits);
     int64_t run = (keys + splits - 1) / splits;
     run = (run + 127) / 128 * 128;
     if (run < 128)
@@ -433,19 +443,31 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
     splits = (keys + run - 1) / run;
     plan.splits = (int)(splits < 1 ? 1 : splits);
     plan.split_keys = (int)(run > INT32_MAX ? INT32_MAX : run);
-    plan.part_rows = rows * num_q_heads * plan.splits;
-    plan.bytes = plan.splits == 1 ? 0 : part * plan.splits;
+    plan.part_rows = (plan.mixed ? narrow : 0) + (plan.splits == 1 ? 0 : rows * num_q_heads * plan.splits);
+    plan.bytes = narrow_part + (plan.splits == 1 ? 0 : part * plan.splits);
     return true;
 }
 
 cudaError_t launch_paged_attention(const PagedParams& p, const PagedPlan& plan, int head_dim, cudaStream_t stream)
 {
-    if (plan.kind == kPagedNarrow)
-        return launch_paged_attention_narrow(p, head_dim, stream);
+    PagedParams few = p;
+    few.narrow_rows = plan.kind == kPagedNarrow ? INT32_MAX : kNarrowRows;
+    if (plan.kind == kPagedNarrow || plan.mixed) {
+        const cudaError_t e = launch_paged_attention_narrow(few, plan.mixed, head_dim, stream);
+        if (e != cudaSuccess || plan.kind == kPagedNarrow)
+            return e;
+    }
+    PagedParams many = p;
+    many.skip_rows = plan.mixed ? kNarrowRows : 0;
+    if (plan.mixed) {
+        const int64_t slots = paged_narrow_slots(head_dim);
+        many.part_o += slots * head_dim;
+        many.part_ml += slots;
+    }
     switch (head_dim) {
-    case 64: return launch_d<64>(p, plan, stream);
-    case 128: return launch_d<128>(p, plan, stream);
-    case 256: return launch_d<256>(p, plan, stream);
+    case 64: return launch_d<64>(many, plan, stream);
+    case 128: return launch_d<128>(many, plan, stream);
+    case 256: return launch_d<256>(many, plan, stream);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -31,7 +31,8 @@ template <int D>
 struct NShape {
     // A stage is 32 KB of keys and values (D 64, 128 and 256: 128, 64 and 32
     // keys), 16 keys per warp and more where a row is short; two stages and
-    // three blocks per SM.  NFIG
+    // three blocks per SM (48 ragged requests, 40 q and 8 key heads of 128: 239 us
+    // with three stages and two blocks, 415 with four and one).
     static constexpr int kWarps = D == 256 ? 2 : 4;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kKeys = 8192 / D;
@@ -73,6 +74,8 @@ __device__ __forceinline__ Listed list_seq(const PagedParams& p, int b)
     // a sequence that does not lie inside the buffer is skipped
     if (s.row0 < 0 || s.ordinal0 < 0 || s.n <= 0 || (long long)s.row0 + s.n > p.pk.num_rows_padded ||
         (long long)s.ordinal0 + s.n > p.pk.num_rows_padded)
+        return Listed{};
+    if ((long long)s.n * p.group > p.narrow_rows)
         return Listed{};
     s.kv_end = (int)min((long long)s.kv_len, (long long)p.max_pages * p.page_size);
     s.q_tiles = (int)(((long long)s.n * p.group + kNRows - 1) / kNRows);
@@ -419,18 +422,25 @@ __global__ void __launch_bounds__(NShape<D>::kThreads) paged_narrow_kernel(const
 // The parts of the triples that several runs share, joined: one warp per (row,
 // head); rows of whole triples are done.
 template <int D>
-__global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_constant__ PagedParams p)
+__global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_constant__ PagedParams p, int tokens)
 {
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const long long task = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int v = (int)(task / p.num_q_heads), head = (int)(task - (long long)v * p.num_q_heads);
     RowSlot s;
-    if (!map_valid_row(v, p.pk.cu_seqlens, p.pk.cu_seqlens_padded, p.pk.num_seqs, p.pk.num_rows_padded, lane, s))
+    if (tokens > 0) {  // of a mixed batch: token v % tokens of sequence v / tokens
+        s.seq = v / tokens;
+        s.local = v - s.seq * tokens;
+        if (s.seq >= p.pk.num_seqs)
+            return;
+    } else if (!map_valid_row(v, p.pk.cu_seqlens, p.pk.cu_seqlens_padded, p.pk.num_seqs, p.pk.num_rows_padded, lane, s)) {
         return;
+    }
     const Listed ls = list_seq<D>(p, s.seq);
-    if (ls.n == 0)
+    if (s.local >= ls.n)
         return;
+    s.row = ls.row0 + s.local;
     const long long run = run_length<D>(listed_before<D>(p, p.pk.num_seqs, lane));
     const int row = s.local * p.group + head % p.group, r = row % kNRows;
     const long long first = listed_before<D>(p, s.seq, lane) +
@@ -479,7 +489,7 @@ __global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_con
 }
 
 template <int D>
-cudaError_t launch_n(const PagedParams& p, cudaStream_t stream)
+cudaError_t launch_n(const PagedParams& p, bool mixed, cudaStream_t stream)
 {
     using S = NShape<D>;
     cudaError_t e = cudaFuncSetAttribute(paged_narrow_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
@@ -487,8 +497,9 @@ cudaError_t launch_n(const PagedParams& p, cudaStream_t stream)
         e = launch_kernel(paged_narrow_kernel<D>, dim3(S::kBlocks), S::kThreads, S::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
-    const long long warps = (long long)p.pk.num_rows_padded * p.num_q_heads;
-    return launch_kernel(paged_narrow_join_kernel<D>, dim3((unsigned)((warps + 3) / 4)), 128, 0, stream, p);
+    const int tokens = mixed ? (kNarrowRows + p.group - 1) / p.group : 0;
+    const long long warps = (mixed ? (long long)p.pk.num_seqs * tokens : p.pk.num_rows_padded) * p.num_q_heads;
+    return launch_kernel(paged_narrow_join_kernel<D>, dim3((unsigned)((warps + 3) / 4)), 128, 0, stream, p, tokens);
 }
 
 }  // namespace
@@ -499,12 +510,12 @@ int64_t paged_narrow_slots(int head_dim)
                                                                                          : NShape<256>::kBlocks));
 }
 
-cudaError_t launch_paged_attention_narrow(const PagedParams& p, int head_dim, cudaStream_t stream)
+cudaError_t launch_paged_attention_narrow(const PagedParams& p, bool mixed, int head_dim, cudaStream_t stream)
 {
     switch (head_dim) {
-    case 64: return launch_n<64>(p, stream);
-    case 128: return launch_n<128>(p, stream);
-    case 256: return launch_n<256>(p, stream);
+    case 64: return launch_n<64>(p, mixed, stream);
+    case 128: return launch_n<128>(p, mixed, stream);
+    case 256: return launch_n<256>(p, mixed, stream);
     default: return cudaErrorInvalidValue;
     }
 }

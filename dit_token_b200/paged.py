@@ -11,6 +11,7 @@ that device's current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Optional, Sequence
@@ -260,11 +261,14 @@ def dit_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
         raise TypeError(f"lse: expected a contiguous float32 CUDA tensor [{rows}, {num_q_heads}]")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise TypeError("workspace: expected a contiguous uint8 CUDA tensor")
+    if not 0 <= window < 2**31:
+        raise ValueError("window: expected 0 (none) or a number of tokens below 2**31")
     scale = 1.0 / math.sqrt(head_dim) if softmax_scale is None else float(softmax_scale)
     on = _stream_on(dev, stream)
     if out is None or (workspace is None and rows > 0 and B > 0):
         # what is allocated here belongs to the stream that uses it
-        with torch.cuda.device(dev), torch.cuda.stream(torch.cuda.ExternalStream(on, device=dev)):
+        with torch.cuda.device(dev), (contextlib.nullcontext() if stream is None else
+                                      torch.cuda.stream(torch.cuda.ExternalStream(on, device=dev))):
             if out is None:
                 out = torch.empty((rows, num_q_heads * head_dim), dtype=q.dtype, device=q.device)
             if workspace is None:

@@ -155,6 +155,7 @@ DIT_API dit_status dit_qkv_rope_append(const void* q, int64_t q_row_stride, cons
  * kv_lens       device int32 [num_seqs]; a negative entry is read as 0
  * num_q_heads   a multiple of num_kv_heads
  * softmax_scale finite, > 0 (usually 1 / sqrt(head_dim))
+ * max_pages     max_pages * page_size at most 2^31 - 4097 (else DIT_ERR_UNSUPPORTED)
  * max_chunk     longest chunk of the batch, max_kv_len the longest kv_lens, where the
  *               host knows them (<= 0: num_rows_padded, max_pages * page_size).
  *               They choose kernels and how the key axis is split; the result

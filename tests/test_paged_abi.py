@@ -172,6 +172,7 @@ def test_attention_refusals(L):
     assert attend(L, hq=3) == SHAPE and attend(L, hq=0) == SHAPE and attend(L, hk=0) == SHAPE
     assert attend(L, d=96) == UNSUP and attend(L, hk=65536, hq=65536, qs=65536 * 128, os=65536 * 128) == UNSUP
     assert attend(L, scale=0.0) == SHAPE and attend(L, scale=math.nan) == SHAPE and attend(L, scale=math.inf) == SHAPE
+    assert attend(L, mp=1 << 27, ts=1 << 27) == UNSUP  # 2^31 keys
     assert attend(L, window=-1) == SHAPE and attend(L, wb=-1) == SHAPE and attend(L, page=0) == SHAPE
     assert attend(L, lse=P + 2) == ALIGN and attend(L, kl=P + 2) == ALIGN
     assert attend(L, B=0, q=None) == OK and attend(L, rows=0, out=None) == OK

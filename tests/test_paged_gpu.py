@@ -11,6 +11,7 @@ from _paged import (Batch, check_attention, check_rotation, cumulative, ints, re
                     reference_rotation)
 
 pytestmark = pytest.mark.gpu
+NAN = math.nan
 
 def attend(x, causal=True, window=0, hints=True, lse=True, **kw):
     """dit_paged_attention on a batch, with canaries around what it may write."""
@@ -190,6 +191,62 @@ def test_offsets_past_32_bits():
     where = x.place(0, 70, 200)
     assert torch.equal(x.v_cache[where].flatten(1), x.v[:130])
     assert torch.equal(x.k_cache[far[3]], before[0]) and torch.equal(x.v_cache[1], before[1])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hk", [(8, 2), (40, 1)])
+def test_next_tokens_beside_chunks(d, hq, hk):
+    """A mixed batch: chunks, chunks of few rows and single tokens, with long
+    caches and without, more key tiles than blocks and fewer."""
+    chunks = [1, 300, 1, 8, 9, 1, 0, 33, 2]
+    pasts = [9000, 500, 0, 700, 64, 4000, 10, 0, 2500]
+    x = Batch(chunks, pasts, hq, hk, d, seed=d).fill()
+    for causal, window in ((True, 0), (False, 0), (True, 300)):
+        attend_and_check(x, causal, window)
+
+
+def test_caches_of_other_strides():
+    """Keys and values in one tensor, heads of a wider cache, pages with slack
+    between them (whose stride is no multiple of a slot's), heads apart from
+    both: what TMA can follow and what it cannot."""
+    for n in (1, 150):
+        for make in ("one tensor", "wider heads", "slack", "loose heads"):
+            x = Batch([n, 2], [200, 70], 4, 2, 128, page=32, seed=22)
+            pages, page, hk, d = x.k_cache.shape
+            if make == "one tensor":
+                both = torch.full((pages, 2, page, hk, d), NAN, dtype=torch.bfloat16, device="cuda")
+                x.k_cache, x.v_cache = both[:, 0], both[:, 1]
+            else:
+                size, strides = {
+                    "wider heads": (page * (hk + 3) * d, (page * (hk + 3) * d, (hk + 3) * d, d, 1)),
+                    "slack": (page * hk * d + 8, (page * hk * d + 8, hk * d, d, 1)),
+                    "loose heads": (page * hk * d * 3, (page * hk * d * 3, d + 8, page * (d + 8) + 16, 1)),
+                }[make]
+                x.k_cache, x.v_cache = (torch.full((pages * size,), NAN, dtype=torch.bfloat16, device="cuda").as_strided(
+                    (pages, page, hk, d), strides) for _ in range(2))
+            x.fill()
+            attend_and_check(x)
+            freqs, _ = dit.dit_rope_frequencies(64)
+            v = x.v.clone()
+            dit.dit_qkv_rope_append(x.q, x.k, x.v, x.k_cache, x.v_cache, x.table, ints(x.pasts), x.cs, x.cp, freqs=freqs,
+                                    q_out=torch.empty_like(x.q), **x.sizes())
+            assert torch.equal(x.v_cache[x.place(0, 200, 200 + n)].flatten(1), v[:n])
+            attend_and_check(x)
+
+
+def test_captured_without_a_workspace():
+    """The workspace and the output come from the graph's own pool."""
+    x = Batch([1, 200], [3000, 500], 8, 2, 128, seed=23).fill()
+    want, _ = attend(x, hints=False)
+    lens = x.kv_lens()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = dit.dit_paged_attention(x.q, x.k_cache, x.v_cache, x.table, lens, x.cs, x.cp, **x.sizes())
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out[x.valid()], want[x.valid()])
 
 
 @pytest.mark.parametrize("n", [1, 260])
@@ -472,6 +529,9 @@ def test_refusals_with_tensors():
     with pytest.raises(TypeError):
         dit.dit_qkv_rope_append(x.q, x.k, x.v, x.k_cache, x.v_cache, x.table, x.kv_lens()[:0], x.cs, x.cp, freqs=freqs,
                                 **x.sizes())
+    for window in (-1, 2**31, 2**32):
+        with pytest.raises(ValueError):
+            dit.dit_paged_attention(*args, window=window, **x.sizes())
     long = Batch([1], [30000], 8, 1, 64, page=64).fill()
     with pytest.raises(dit.DitError):
         dit.dit_paged_attention(long.q, long.k_cache, long.v_cache, long.table, long.kv_lens(), long.cs, long.cp,
