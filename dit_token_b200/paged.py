@@ -18,7 +18,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import _call, _offsets, _packing, _rows, _vec
+from . import _call, _packing, _rows
 
 _ROPE_MODES = {"interleaved": 0, "half": 1, "none": 2}
 _ROPE_SCALES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
@@ -58,15 +58,23 @@ def _call_on(index: int, name: str, *args) -> None:
             _call(name, *args)
 
 
+def _pack(cu_seqlens: torch.Tensor, cu_seqlens_padded: torch.Tensor) -> tuple:
+    n = cu_seqlens.shape
+    if cu_seqlens.dtype is torch.int32 and cu_seqlens_padded.dtype is torch.int32 and len(n) == 1 and n[0] > 0 and \
+            cu_seqlens_padded.shape == n and cu_seqlens.is_contiguous() and cu_seqlens_padded.is_contiguous():
+        return cu_seqlens.data_ptr(), cu_seqlens_padded.data_ptr(), n[0] - 1
+    return _packing(cu_seqlens, cu_seqlens_padded)  # says what is wrong
+
+
 def _ints(t: torch.Tensor, shape: tuple, what: str) -> int:
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{what}: expected a contiguous int32 CUDA tensor {list(shape)}")
     return t.data_ptr() or None
 
 
 def _freqs(t: torch.Tensor, n: Optional[int], what: str) -> int:
-    if t.dtype != torch.float64 or not t.is_cuda or t.dim() != 1 or not t.is_contiguous() or \
-            (n is not None and t.numel() != n):
+    shape = t.shape
+    if t.dtype is not torch.float64 or len(shape) != 1 or not t.is_contiguous() or (n is not None and shape[0] != n):
         raise TypeError(f"{what}: expected a contiguous float64 CUDA vector"
                         + ("" if n is None else f" of {n} entries"))
     return t.data_ptr()
@@ -74,10 +82,12 @@ def _freqs(t: torch.Tensor, n: Optional[int], what: str) -> int:
 
 def _heads(t: torch.Tensor, heads: int, head_dim: int, rows: int, what: str) -> tuple:
     """(pointer, row stride) of [rows, heads * head_dim] or [rows, heads, head_dim]."""
-    if t.dim() == 2 and t.dtype == torch.bfloat16 and t.is_cuda and (t.stride(1) == 1 or t.size(1) == 1):
-        ptr, stride = t.data_ptr(), t.stride(0)
-    else:
-        ptr, stride = _rows(t, what)
+    width = heads * head_dim
+    if t.dtype is torch.bfloat16 and t.shape == (rows, width):  # the usual case, first
+        st = t.stride()
+        if st[1] == 1:
+            return t.data_ptr(), st[0] if rows > 1 else width
+    ptr, stride = _rows(t, what)
     if t.size(0) != rows or t.numel() != rows * heads * head_dim:
         raise ValueError(f"{what}: expected {rows} rows of {heads} heads of {head_dim}, got {tuple(t.shape)}")
     # one row has no stride of its own: torch may report any
@@ -87,7 +97,7 @@ def _heads(t: torch.Tensor, heads: int, head_dim: int, rows: int, what: str) -> 
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, heads: int, head_dim: int,
            B: int) -> tuple:
     shape = k_cache.shape
-    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16 or not (k_cache.is_cuda and v_cache.is_cuda):
+    if k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16:
         raise TypeError("k_cache, v_cache: expected bfloat16 CUDA tensors")
     if len(shape) != 4 or shape[2] != heads or shape[3] != head_dim or v_cache.shape != shape:
         raise ValueError(f"k_cache, v_cache: expected [pages, page_size, {heads}, {head_dim}], got {tuple(shape)} and "
@@ -104,12 +114,12 @@ def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tens
     ks = strides(ks)
     if ks != strides(vs):
         raise ValueError("k_cache and v_cache must have the same strides")
-    if block_table.dtype != torch.int32 or not block_table.is_cuda or block_table.dim() != 2 or \
-            block_table.size(0) != B or (block_table.size(1) > 1 and block_table.stride(1) != 1):
+    ts, tt = block_table.shape, block_table.stride()
+    if block_table.dtype is not torch.int32 or len(ts) != 2 or ts[0] != B or (ts[1] > 1 and tt[1] != 1):
         raise TypeError("block_table: expected an int32 CUDA tensor [num_seqs, max_pages], contiguous rows")
-    table_stride = block_table.stride(0) if B > 1 else block_table.size(1)
+    table_stride = tt[0] if B > 1 else ts[1]
     return (k_cache.data_ptr() or None, v_cache.data_ptr() or None, *ks, pages, page_size), \
-        (block_table.data_ptr() or None, table_stride, block_table.size(1))
+        (block_table.data_ptr() or None, table_stride, ts[1])
 
 
 def dit_rope_frequencies(rotary_dim: int, *, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -140,7 +150,7 @@ def _rope_args(freqs, rope_grid, grid_freqs, sections, pos_offset, attn_scale, e
             if grid_freqs is None:
                 raise TypeError("grid_freqs: needed with rope_grid")
             gf = _freqs(grid_freqs, freqs.numel(), "grid_freqs")
-    po = None if pos_offset is None else _offsets(pos_offset, B)
+    po = None if pos_offset is None else _ints(pos_offset, (B,), "pos_offset")
     return fp, rotary, gp, gf, st, sh, sw, po, float(attn_scale), float(eps), mode
 
 
@@ -150,9 +160,11 @@ def _weights(q_weight, k_weight, head_dim):
     if q_weight is None:
         return None, None
     for t, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t.dtype is not torch.bfloat16:
+            raise TypeError(f"{what}: expected bfloat16, got {t.dtype}")
         if t.numel() != head_dim or not t.is_contiguous():
             raise ValueError(f"{what}: expected a contiguous vector of {head_dim}")
-    return _vec(q_weight, "q_weight"), _vec(k_weight, "k_weight")
+    return q_weight.data_ptr(), k_weight.data_ptr()
 
 
 def dit_qk_rope_scaled(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tensor, cu_seqlens_padded: torch.Tensor,
@@ -178,7 +190,7 @@ def dit_qk_rope_scaled(q: torch.Tensor, k: torch.Tensor, cu_seqlens: torch.Tenso
     kp, ks = _heads(k, num_k_heads, head_dim, rows, "k")
     qop, qos = _heads(qo, num_q_heads, head_dim, rows, "q_out")
     kop, kos = _heads(ko, num_k_heads, head_dim, rows, "k_out")
-    cs, cp, B = _packing(cu_seqlens, cu_seqlens_padded)
+    cs, cp, B = _pack(cu_seqlens, cu_seqlens_padded)
     wq, wk = _weights(q_weight, k_weight, head_dim)
     fp, rotary, gp, gf, st, sh, sw, po, gain, eps, mode = _rope_args(
         freqs, rope_grid, grid_freqs, sections, pos_offset, attn_scale, eps, rope_mode, B)
@@ -211,7 +223,7 @@ def dit_qkv_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cac
     kp, ks = _heads(k, num_kv_heads, head_dim, rows, "k")
     vp, vs = _heads(v, num_kv_heads, head_dim, rows, "v")
     qop, qos = _heads(qo, num_q_heads, head_dim, rows, "q_out")
-    cs, cp, B = _packing(cu_seqlens, cu_seqlens_padded)
+    cs, cp, B = _pack(cu_seqlens, cu_seqlens_padded)
     wq, wk = _weights(q_weight, k_weight, head_dim)
     cache, table = _cache(k_cache, v_cache, block_table, num_kv_heads, head_dim, B)
     fp, rotary, gp, gf, st, sh, sw, po, gain, eps, mode = _rope_args(
@@ -253,7 +265,7 @@ def dit_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     rows = q.size(0)
     dev = _one_device(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, cu_seqlens_padded, out, lse, workspace)
     qp, qs = _heads(q, num_q_heads, head_dim, rows, "q")
-    cs, cp, B = _packing(cu_seqlens, cu_seqlens_padded)
+    cs, cp, B = _pack(cu_seqlens, cu_seqlens_padded)
     cache, table = _cache(k_cache, v_cache, block_table, num_kv_heads, head_dim, B)
     lens = _ints(kv_lens, (B,), "kv_lens")
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous()
