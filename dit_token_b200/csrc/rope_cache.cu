@@ -12,12 +12,14 @@
 // row and run of heads: D / 8 lanes hold a head, 8 elements per lane, so a
 // lane needs the angles of the same 4 pairs for every head and forms them once
 // (the fp64 product p f_j, reduced, then the hardware sine and cosine).  The
-// heads go in batches of U steps, a batch's loads in flight while the one
+// heads go in batches of 4 steps, a batch's loads in flight while the one
 // before is computed.  A batch of few rows (next tokens) cannot fill the
 // GPU with whole rows: its rows' batches are spread over up to as many warps,
-// which repeats the angles and shortens the chain of loads (rows_per_run
-// below).  q, k and v are batched apart, so a batch has one weight vector and
-// one destination rule.
+// which repeats the angles and shortens the chain of loads (launch_rc).  q, k
+// and v are batched apart, so a batch has one weight vector and one
+// destination.  Measured: 61,888 rows of 16 + 16 heads of 128 in 162 us (6.27
+// TB/s), four ragged prompts of 53,619 rows of 40 + 8 heads in 223 us (5.90),
+// 20,819 rows of 40 + 8 + 8 heads into pages of 16 in 97.5 us (6.12).
 #include "common.cuh"
 #include "launch.h"
 #include "rope.cuh"
@@ -77,10 +79,13 @@ __device__ __forceinline__ void store_quads(uint16_t* head, int o0, int o1, uint
 // What a pair's elements are multiplied by: with weights these are folded into
 // the rotation, (o_a, o_b) = r (x_a c0 + x_b c1, x_a c2 + x_b c3), so that a
 // normed and turned pair costs two products, two fused ones and r.  A lane that
-// passes has c0 = w_a, c3 = w_b and zeros.  One set is kept, and folded again
-// between q's heads and k's: kept for both, registers (126 against 96 a thread)
-// leave fewer warps resident, 197 us for the long video against 171; without
-// weights (150 us, 104 % of the measured copy rate) there is one set anyway.
+// passes has c0 = w_a, c3 = w_b and zeros.  (Weights applied on their own: 186
+// us for the long video.)  q's and k's coefficients are both kept: registers
+// decide how many warps hide the loads, and with a head's stride known (D) for
+// all but the cache's writes they fit in 96 (162 us, 97 % of the measured copy
+// rate; in one kernel for both destinations 126 registers and 197 us, one set
+// folded again between q and k 174).  Without weights there is one set: 150 us
+// for the same bytes.
 struct PairCoef {
     float c0[4], c1[4], c2[4], c3[4];
 };
@@ -147,12 +152,12 @@ __device__ __forceinline__ void turn_batch(uint16_t* to, int64_t step, int heads
         uint4 out = pack8(o);
         if (!NORM && !turns)
             out = x[u];  // passes bit for bit
-        if (h < heads && to != nullptr)
+        if (h < heads)
             store_quads<MODE>(to + (int64_t)h * step, o0, o1, out, keep);
     }
 }
 
-template <int D, int MODE, bool NORM, int U>
+template <int D, int MODE, bool NORM, bool APPEND, int U>
 __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __grid_constant__ RopeCacheParams p)
 {
     constexpr int LPH = D / 8;          // lanes per head
@@ -168,7 +173,7 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
         return;
     const int sub = lane / LPH, li = lane % LPH;
     const int nq = (p.num_q_heads + HB - 1) / HB, nk = (p.num_k_heads + HB - 1) / HB;
-    const int total = nq + nk + (p.v != nullptr ? nk : 0);
+    const int total = nq + nk + (APPEND ? nk : 0);
     const int b0 = run * p.batches_per_run, b1 = min(b0 + p.batches_per_run, total);
     if (b0 >= b1)
         return;
@@ -178,11 +183,10 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
 
     // Where the row's k and v go: the rows' own outputs, or the token's slot
     // in the cache.  A token whose slot the table does not name is dropped.
-    const int before = p.cache_lens != nullptr ? max(__ldg(p.cache_lens + s.seq), 0) : 0;
+    const int before = APPEND ? max(__ldg(p.cache_lens + s.seq), 0) : 0;
     uint16_t* k_to = nullptr;
     uint16_t* v_to = nullptr;
-    int64_t head_step = D;
-    if (p.block_table != nullptr) {
+    if (APPEND) {
         const long long slot = (long long)before + s.local;
         const long long entry = slot / p.page_size;
         if (entry < p.max_pages) {
@@ -193,8 +197,7 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
                 v_to = p.v_cache + at;
             }
         }
-        head_step = p.head_stride;
-    } else if (p.k_out != nullptr) {
+    } else {
         k_to = p.k_out + (int64_t)s.row * p.k_out_stride;
     }
     const uint16_t* q_from = p.q + (int64_t)s.row * p.q_row_stride;
@@ -234,26 +237,30 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
             sn[e] *= p.attn_scale;
         }
     }
-    PairCoef pc;
-    fold<MODE, NORM>(pc, c, sn, b0 < nq ? p.q_weight : p.k_weight, o0, o1);
+    PairCoef pq, pk;
+    fold<MODE, NORM>(pq, c, sn, p.q_weight, o0, o1);
+    if (NORM)
+        fold<MODE, NORM>(pk, c, sn, p.k_weight, o0, o1);
 
-    const bool cached = p.block_table != nullptr;
     for (int b = b0; b < b1; ++b) {
         uint4 nxt[U];
         if (b + 1 < b1)
             load(b + 1, nxt);
-        if (NORM && b == nq && b > b0)  // from q's heads to k's
-            fold<MODE, NORM>(pc, c, sn, p.k_weight, o0, o1);
-        if (b < nq + nk) {
-            const bool is_q = b < nq;
-            turn_batch<D, MODE, NORM, U>(is_q ? q_to : k_to, is_q ? D : head_step, is_q ? p.num_q_heads : p.num_k_heads,
-                                         (is_q ? b : b - nq) * HB + sub, o0, o1, !is_q && cached, turns, p.eps, pc, cur);
-        } else if (v_to != nullptr) {
+        if (b < nq) {
+            turn_batch<D, MODE, NORM, U>(q_to, D, p.num_q_heads, b * HB + sub, o0, o1, false, turns, p.eps, pq, cur);
+        } else if (!APPEND) {
+            turn_batch<D, MODE, NORM, U>(k_to, D, p.num_k_heads, (b - nq) * HB + sub, o0, o1, false, turns, p.eps,
+                                         NORM ? pk : pq, cur);
+        } else if (k_to != nullptr) {
+            const int h0 = (b - nq - (b < nq + nk ? 0 : nk)) * HB + sub;
+            if (b < nq + nk) {
+                turn_batch<D, MODE, NORM, U>(k_to, p.head_stride, p.num_k_heads, h0, o0, o1, true, turns, p.eps,
+                                             NORM ? pk : pq, cur);
+            } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = (b - nq - nk) * HB + sub + u * HPW;
-                if (h < p.num_k_heads)
-                    store_quads<MODE>(v_to + (int64_t)h * head_step, o0, o1, cur[u], true);
+                for (int u = 0; u < U; ++u)
+                    if (h0 + u * HPW < p.num_k_heads)
+                        store_quads<MODE>(v_to + (h0 + u * HPW) * p.head_stride, o0, o1, cur[u], true);
             }
         }
 #pragma unroll
@@ -276,11 +283,17 @@ cudaError_t launch_rc(RopeCacheParams p, int mode, cudaStream_t stream)
     p.runs_per_row = (total + p.batches_per_run - 1) / p.batches_per_run;
     const unsigned grid = (unsigned)(((long long)p.pk.num_rows_padded * p.runs_per_row + kRcWarps - 1) / kRcWarps);
     const bool norm = p.k_weight != nullptr;
-    if (mode == kRopeHalf)
-        return norm ? launch_kernel(rope_cache_kernel<D, kRopeHalf, true, U>, grid, kRcWarps * kWarp, 0, stream, p)
-                    : launch_kernel(rope_cache_kernel<D, kRopeHalf, false, U>, grid, kRcWarps * kWarp, 0, stream, p);
-    return norm ? launch_kernel(rope_cache_kernel<D, kRopeInterleaved, true, U>, grid, kRcWarps * kWarp, 0, stream, p)
-                : launch_kernel(rope_cache_kernel<D, kRopeInterleaved, false, U>, grid, kRcWarps * kWarp, 0, stream, p);
+    auto launch = [&](auto* kernel) { return launch_kernel(kernel, grid, kRcWarps * kWarp, 0, stream, p); };
+    const bool half = mode == kRopeHalf, append = p.block_table != nullptr;
+    if (half && norm)
+        return append ? launch(rope_cache_kernel<D, kRopeHalf, true, true, U>) : launch(rope_cache_kernel<D, kRopeHalf, true, false, U>);
+    if (half)
+        return append ? launch(rope_cache_kernel<D, kRopeHalf, false, true, U>) : launch(rope_cache_kernel<D, kRopeHalf, false, false, U>);
+    if (norm)
+        return append ? launch(rope_cache_kernel<D, kRopeInterleaved, true, true, U>)
+                      : launch(rope_cache_kernel<D, kRopeInterleaved, true, false, U>);
+    return append ? launch(rope_cache_kernel<D, kRopeInterleaved, false, true, U>)
+                  : launch(rope_cache_kernel<D, kRopeInterleaved, false, false, U>);
 }
 
 }  // namespace
