@@ -207,7 +207,7 @@ struct PagedParams {
 // A cache whose strides make it a matrix of rows slot_stride apart: slot s of
 // page g, head h is row g * page_rows + s + h * head_rows, columns from
 // h * head_cols.  box_rows: the largest power of two, at most 128, that divides
-// the page size.  false: its strides do not, or the page size is no multiple of 8.
+// the page size.  false: its strides do not, or the page size is no multiple of 4.
 struct CacheRows {
     int32_t page_rows, head_rows, head_cols, box_rows;
     int64_t rows, cols;

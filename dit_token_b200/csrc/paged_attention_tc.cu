@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                     mbar_expect(full(slot), boxes * (uint32_t)box * (D * 2));
                 __syncwarp();
                 if (there) {
-                    const uint32_t to = base + S::kRing + slot * S::kTile + (uint32_t)(lane * (box / 8)) * S::kGroup;
+                    const uint32_t to = base + S::kRing + slot * S::kTile + (uint32_t)lane * (WHOLE ? S::kGroup : (uint32_t)box * 128);
                     const CUtensorMap* map = (j & 1) ? &v_map : &k_map;
                     if (WHOLE) {
                         tma_box3(to, map, row, x / 64, full(slot));
@@ -719,7 +719,7 @@ cudaError_t launch_tc(const PagedParams& p, int tiles, cudaStream_t stream)
         return cudaErrorInvalidValue;
     // whole heads where they make fewer boxes of a tile
     if constexpr (D > 64)
-        if (kTcKeys / c.box_rows * (D / 64) > kTcKeys / 8 && c.head_cols % 64 == 0)
+        if (c.box_rows >= 8 && kTcKeys / c.box_rows * (D / 64) > kTcKeys / 8 && c.head_cols % 64 == 0)
             return launch_tc_boxes<D, true>(p, c, tiles, stream);
     return launch_tc_boxes<D, false>(p, c, tiles, stream);
 }
@@ -730,7 +730,7 @@ bool cache_rows(int64_t page_stride, int64_t slot_stride, int64_t head_stride, i
                 int num_kv_heads, int head_dim, CacheRows& c)
 {
     const int64_t pages = num_pages > 0 ? num_pages : 1;
-    if (page_size % 8 != 0)
+    if (page_size % 4 != 0)  // 32 boxes of a tile, one per lane of the fetching warp
         return false;
     int64_t head_rows = 0, head_cols = 0;
     if (num_kv_heads > 1) {  // heads lie within a row (slot-major pages) or whole rows apart (head-major)

@@ -55,7 +55,7 @@ def test_head_groups(hq, hk, n):
     attend_and_check(Batch([n, n], [100, 5], hq, hk, 64, seed=hq).fill())
 
 
-@pytest.mark.parametrize("page", [1, 7, 16, 100, 256])
+@pytest.mark.parametrize("page", [1, 7, 10, 12, 16, 20, 100, 256])
 @pytest.mark.parametrize("chunks,pasts", [([1, 1, 1], [0, 99, 255]), ([130, 1, 40], [70, 256, 0])])
 def test_page_sizes(page, chunks, pasts):
     attend_and_check(Batch(chunks, pasts, 4, 2, 128, page=page, seed=page).fill())
