@@ -16,19 +16,25 @@
 //                   row maxima and sums need no exchange
 //   warp 8          issues the products: s = q k^T (both from shared memory)
 //                   and o += p v (p from tensor memory)
-//   warp 9          fetches k and v with TMA, in boxes of rows that never cross
-//                   a page: the largest power of two that divides the page
-//                   size, 8 to 128 rows; and writes zeros over the last step's
-//                   rows of v behind the block's keys: the cache may hold
-//                   anything behind the last token, and 0 * NaN must not reach
-//                   the sums
+//   warp 9, warp 10 fetch k and v with TMA, in boxes of rows that never cross a
+//                   page: of 64 elements, the largest power of two rows that
+//                   divides the page size, 4 to 128, or of whole heads, 8 rows,
+//                   where those are fewer; warp 10 also writes zeros over the
+//                   last step's rows of v behind the block's keys: the cache may
+//                   hold anything behind the last token, and 0 * NaN must not
+//                   reach the sums
+// A box costs its warp some 40 cycles, whatever it holds.  (Heads of 256 in
+// pages of 40: 154 us in boxes of 64 elements, 92 in whole heads, 81 by two
+// warps; the video chunk in pages of 100, boxes of 4 rows: 5936 us by one warp,
+// 3252 by two.)
 // The softmax warps first copy q.  (Fetching k and v with 16-byte asynchronous
 // copies by three warps held the video chunk at 3584 us, 2.8 us a step, and
 // gathering TMA copies of four rows at 6210; without any copies it took 2611.)
 // Steps begin at multiples of 128 keys, so boxes keep their alignment.
 // The two tiles alternate: while one's softmax runs, the other's products do.
 // Tensor memory (512 columns of 128 lanes x 32 bits): s0, s1 (128 each), o0,
-// o1 (D each; heads of 256 leave room for one tile per block); p takes the second half of its s, once the row is in registers.
+// o1 (D each; heads of 256 leave room for one tile per block); p takes the
+// second half of its s, once the row is in registers.
 // The products of one tile are issued in the order o(i), s(i+1), and a
 // commit covers everything issued before it, so "s(i+1) is there" also says
 // that o(i) is complete and p(i) is free.
@@ -446,7 +452,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 }
                 __syncwarp();
             }
-        } else if (warp == 9) {
+        } else if (warp < 11) {
+            const int of_v = warp - 9;  // 0: k, 1: v
+            const CUtensorMap* map = of_v ? &v_map : &k_map;
             // Lane e fetches the box of rows e * box of every tile, where there
             // is one.  Page numbers are read a step ahead.
             const int32_t* table = p.block_table + (int64_t)q.seq * p.table_stride;
@@ -465,16 +473,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             };
             if (steps > 0)
                 look_up(0);
-            int j = 0;
-            for (; j < 2 * steps; ++j) {
-                const int slot = j % NS;
-                if ((j & 1) == 0) {
-                    there = next;
-                    // a page outside the cache: rows outside the map, which read as zeros
-                    row = page >= 0 && page < p.num_pages ? page * p.page_rows + slot_in + head_row : -kTcKeys;
-                    if (j / 2 + 1 < steps)
-                        look_up(j / 2 + 1);
-                }
+            int i = 0;
+            for (; i < steps; ++i) {
+                const int j = 2 * i + of_v, slot = j % NS;
+                there = next;
+                // a page outside the cache: rows outside the map, which read as zeros
+                row = page >= 0 && page < p.num_pages ? page * p.page_rows + slot_in + head_row : -kTcKeys;
+                if (i + 1 < steps)
+                    look_up(i + 1);
                 if (j >= NS && !__all_sync(0xffffffffu, mbar_wait(empty(slot), (uint32_t)(j / NS - 1) & 1u, abort)))
                     break;
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, there));
@@ -483,7 +489,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 __syncwarp();
                 if (there) {
                     const uint32_t to = base + S::kRing + slot * S::kTile + (uint32_t)lane * (WHOLE ? S::kGroup : (uint32_t)box * 128);
-                    const CUtensorMap* map = (j & 1) ? &v_map : &k_map;
                     if (WHOLE) {
                         tma_box3(to, map, row, x / 64, full(slot));
                     } else {
@@ -496,9 +501,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             }
             // The last tile of v: this warp has seen the slot's previous use end,
             // so the parity it waits for is the tile's own.
-            if (j == 2 * steps && behind < kTcKeys && steps > 0) {
-                const int slot = (j - 1) % NS;
-                if (__all_sync(0xffffffffu, mbar_wait(full(slot), (uint32_t)((j - 1) / NS) & 1u, abort))) {
+            if (of_v && i == steps && behind < kTcKeys && steps > 0) {
+                const int j = 2 * steps - 1, slot = j % NS;
+                if (__all_sync(0xffffffffu, mbar_wait(full(slot), (uint32_t)(j / NS) & 1u, abort))) {
                     for (int c = 0; c < D / 64; ++c)
                         for (int e = behind * 8 + lane; e < kTcKeys * 8; e += 32) {
                             const int r = e >> 3;
@@ -513,11 +518,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 }
             }
             // given up: let the copies under way land before the block ends
-            if (j < 2 * steps && lane == 0) {
+            if (i < steps && lane == 0) {
                 const long long from = clock64();
-                for (int e = max(j - NS, 0); e < j; ++e)
-                    while (!mbar_try(full(e % NS), (uint32_t)(e / NS) & 1u) && clock64() - from < kWaitCycles) {
+                for (int e = max(i - NS / 2, 0); e < i; ++e) {
+                    const int j = 2 * e + of_v;
+                    while (!mbar_try(full(j % NS), (uint32_t)(j / NS) & 1u) && clock64() - from < kWaitCycles) {
                     }
+                }
             }
         }
     } else {
