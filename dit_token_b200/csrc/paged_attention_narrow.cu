@@ -136,11 +136,57 @@ __device__ __forceinline__ int find_listed(const PagedParams& p, long long at, i
     return -1;
 }
 
+// Quotient of counts that nearly always fit 32 bits.
+__device__ __forceinline__ long long div_count(long long a, long long b)
+{
+    return ((unsigned long long)(a | b) >> 31) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+__device__ __forceinline__ Listed shfl_listed(const Listed& s, int src)
+{
+    Listed r;
+    r.n = __shfl_sync(0xffffffffu, s.n, src);
+    r.row0 = __shfl_sync(0xffffffffu, s.row0, src);
+    r.ordinal0 = __shfl_sync(0xffffffffu, s.ordinal0, src);
+    r.kv_len = __shfl_sync(0xffffffffu, s.kv_len, src);
+    r.kv_end = __shfl_sync(0xffffffffu, s.kv_end, src);
+    r.q_tiles = __shfl_sync(0xffffffffu, s.q_tiles, src);
+    r.lo = __shfl_sync(0xffffffffu, s.lo, src);
+    r.k_tiles = __shfl_sync(0xffffffffu, s.k_tiles, src);
+    return r;
+}
+
+// The whole list of a batch of up to 32 sequences, one per lane, read in one
+// round: a few next tokens are bound by such rounds (the one-token call 16.5
+// us with three of them before its first key, 15.8 with one).
+struct WholeList {
+    Listed mine;
+    long long before;  // entries before the lane's sequence
+    long long total;
+};
+template <int D>
+__device__ __forceinline__ WholeList whole_list(const PagedParams& p, int lane)
+{
+    WholeList w;
+    w.mine = list_seq<D>(p, lane);
+    const long long c = w.mine.count(p);
+    long long sum = c;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+        const long long up = (long long)__shfl_up_sync(0xffffffffu, (unsigned long long)sum, o);
+        if (lane >= o)
+            sum += up;
+    }
+    w.before = sum - c;
+    w.total = shfl_ll(sum, kWarp - 1);
+    return w;
+}
+
 // Entries per block: an equal share, and two tiles at least.
 template <int D>
 __device__ __forceinline__ long long run_length(long long total)
 {
-    const long long share = (total + NShape<D>::kBlocks - 1) / NShape<D>::kBlocks;
+    const long long share = div_count(total + NShape<D>::kBlocks - 1, NShape<D>::kBlocks);
     return share > 2 ? share : 2;
 }
 
@@ -153,7 +199,11 @@ __global__ void __launch_bounds__(NShape<D>::kThreads) paged_narrow_kernel(const
     extern __shared__ __align__(128) unsigned char smem[];
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long total = listed_before<D>(p, p.pk.num_seqs, lane);
+    const bool few = p.pk.num_seqs <= kWarp;
+    WholeList w{};
+    if (few)
+        w = whole_list<D>(p, lane);
+    const long long total = few ? w.total : listed_before<D>(p, p.pk.num_seqs, lane);
     const long long run = run_length<D>(total);
     const long long begin = blockIdx.x * run, end = min(begin + run, total);
     if (begin >= end)
@@ -165,10 +215,20 @@ __global__ void __launch_bounds__(NShape<D>::kThreads) paged_narrow_kernel(const
     const uint32_t a_ring = a_q + S::kQ;
 
     long long at = begin, before;
-    int seq = find_listed<D>(p, at, lane, before);
-    if (seq < 0)
-        return;
-    Listed ls = list_seq<D>(p, seq);
+    int seq;
+    Listed ls;
+    if (few) {
+        seq = __ffs(__ballot_sync(0xffffffffu, at < w.before + w.mine.count(p))) - 1;
+        if (seq < 0)
+            return;
+        before = shfl_ll(w.before, seq);
+        ls = shfl_listed(w.mine, seq);
+    } else {
+        seq = find_listed<D>(p, at, lane, before);
+        if (seq < 0)
+            return;
+        ls = list_seq<D>(p, seq);
+    }
     while (at < end) {
         while (at >= before + ls.count(p)) {  // the next sequence that has entries
             before += ls.count(p);
@@ -176,13 +236,14 @@ __global__ void __launch_bounds__(NShape<D>::kThreads) paged_narrow_kernel(const
                 return;
             ls = list_seq<D>(p, seq);
         }
-        const long long triple = (at - before) / ls.k_tiles;
+        const long long triple = div_count(at - before, ls.k_tiles);
         const int t0 = (int)(at - before - triple * ls.k_tiles);
         const int t1 = (int)min((long long)ls.k_tiles, t0 + (end - at));
-        const int kvh = (int)(triple % p.num_kv_heads);
+        const long long q_tile = div_count(triple, p.num_kv_heads);
+        const int kvh = (int)(triple - q_tile * p.num_kv_heads);
         QueryTile q;
         q.seq = seq;
-        q.first = (int)(triple / p.num_kv_heads) * kNRows;
+        q.first = (int)q_tile * kNRows;
         q.rows = min(kNRows, ls.n * p.group - q.first);
         q.n = ls.n;
         q.row0 = ls.row0;
@@ -428,24 +489,42 @@ __global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_con
     const int lane = threadIdx.x & 31;
     const long long task = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int v = (int)(task / p.num_q_heads), head = (int)(task - (long long)v * p.num_q_heads);
-    RowSlot s;
-    if (tokens > 0) {  // of a mixed batch: token v % tokens of sequence v / tokens
-        s.seq = v / tokens;
-        s.local = v - s.seq * tokens;
-        if (s.seq >= p.pk.num_seqs)
-            return;
-    } else if (!map_valid_row(v, p.pk.cu_seqlens, p.pk.cu_seqlens_padded, p.pk.num_seqs, p.pk.num_rows_padded, lane, s)) {
+    // token `local` of sequence `seq`: of a mixed batch token v % tokens of
+    // sequence v / tokens, else valid row v
+    int seq = tokens > 0 ? v / tokens : -1, local = tokens > 0 ? v - seq * tokens : 0;
+    if (seq >= p.pk.num_seqs)
         return;
+    Listed ls;
+    long long before, total;
+    if (p.pk.num_seqs <= kWarp) {
+        const WholeList w = whole_list<D>(p, lane);
+        if (tokens == 0) {
+            seq = __ffs(__ballot_sync(0xffffffffu, v >= w.mine.ordinal0 && v < w.mine.ordinal0 + w.mine.n)) - 1;
+            if (seq < 0)
+                return;
+            local = v - __shfl_sync(0xffffffffu, w.mine.ordinal0, seq);
+        }
+        ls = shfl_listed(w.mine, seq);
+        before = shfl_ll(w.before, seq);
+        total = w.total;
+    } else {
+        if (tokens == 0) {
+            RowSlot s;
+            if (!map_valid_row(v, p.pk.cu_seqlens, p.pk.cu_seqlens_padded, p.pk.num_seqs, p.pk.num_rows_padded, lane, s))
+                return;
+            seq = s.seq;
+            local = s.local;
+        }
+        ls = list_seq<D>(p, seq);
+        before = listed_before<D>(p, seq, lane);
+        total = listed_before<D>(p, p.pk.num_seqs, lane);
     }
-    const Listed ls = list_seq<D>(p, s.seq);
-    if (s.local >= ls.n)
+    if (local >= ls.n)
         return;
-    s.row = ls.row0 + s.local;
-    const long long run = run_length<D>(listed_before<D>(p, p.pk.num_seqs, lane));
-    const int row = s.local * p.group + head % p.group, r = row % kNRows;
-    const long long first = listed_before<D>(p, s.seq, lane) +
-                            ((long long)(row / kNRows) * p.num_kv_heads + head / p.group) * ls.k_tiles;
-    const int b0 = (int)(first / run), b1 = (int)((first + ls.k_tiles - 1) / run);
+    const long long run = run_length<D>(total);
+    const int row = local * p.group + head % p.group, r = row % kNRows;
+    const long long first = before + ((long long)(row / kNRows) * p.num_kv_heads + head / p.group) * ls.k_tiles;
+    const int b0 = (int)div_count(first, run), b1 = (int)div_count(first + ls.k_tiles - 1, run);
     if (b0 == b1)
         return;
     auto part_of = [&](int b) { return (int64_t)(2 * b + (first < b * run ? 0 : 1)) * kNRows + r; };
@@ -480,12 +559,13 @@ __global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_con
     }
     ll = group_sum<32>(ll);
     const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
-    uint16_t* out = p.out + (int64_t)s.row * p.out_row_stride + head * D + lane * E;
+    const int64_t out_row = ls.row0 + local;
+    uint16_t* out = p.out + out_row * p.out_row_stride + head * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; e += 2)
         *reinterpret_cast<uint32_t*>(out + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
     if (lane == 0 && p.lse != nullptr)
-        p.lse[(int64_t)s.row * p.num_q_heads + head] = (mm + log2f(ll)) * kLn2;
+        p.lse[out_row * p.num_q_heads + head] = (mm + log2f(ll)) * kLn2;
 }
 
 template <int D>
