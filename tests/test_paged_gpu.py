@@ -361,7 +361,8 @@ def test_rotation(mode, d, rotary, norm, grid):
 def test_rotation_head_counts(hq, hk, chunks):
     x, kw, ref = rotation_case("half", 64, 64, max(hq, 1), max(hk, 1), True, False, chunks=chunks)
     ref["starts"] = [0, 0, 0]
-    dit.dit_qk_rope_scaled(x.q[:, :hq * 64], x.k[:, :hk * 64], x.cs, x.cp, num_q_heads=hq, num_k_heads=hk, head_dim=64,
+    q = x.q[:, :hq * 64] if hq else torch.empty(x.rows, 0, dtype=torch.bfloat16, device="cuda")
+    dit.dit_qk_rope_scaled(q, x.k[:, :hk * 64], x.cs, x.cp, num_q_heads=hq, num_k_heads=hk, head_dim=64,
                            q_out=(qo := torch.zeros(x.rows, hq * 64, dtype=torch.bfloat16, device="cuda")),
                            k_out=(ko := torch.zeros(x.rows, hk * 64, dtype=torch.bfloat16, device="cuda")), **kw)
     ok = x.valid()
