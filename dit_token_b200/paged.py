@@ -47,11 +47,12 @@ def _stream_on(index: int, stream) -> int:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call_on(index: int, name: str, *args) -> None:
     """The library launches on the current device; make it the tensors'."""
-    if torch.cuda.current_device() == index:
+    if _raw_device() == index:
         _call(name, *args)
     else:
         with torch.cuda.device(index):
@@ -60,6 +61,10 @@ def _call_on(index: int, name: str, *args) -> None:
 
 def _pack(cu_seqlens: torch.Tensor, cu_seqlens_padded: torch.Tensor) -> tuple:
     n = cu_seqlens.shape
+    if cu_seqlens_padded is cu_seqlens and cu_seqlens.dtype is torch.int32 and len(n) == 1 and n[0] > 0 and \
+            cu_seqlens.is_contiguous():  # nothing is padded
+        p = cu_seqlens.data_ptr()
+        return p, p, n[0] - 1
     if cu_seqlens.dtype is torch.int32 and cu_seqlens_padded.dtype is torch.int32 and len(n) == 1 and n[0] > 0 and \
             cu_seqlens_padded.shape == n and cu_seqlens.is_contiguous() and cu_seqlens_padded.is_contiguous():
         return cu_seqlens.data_ptr(), cu_seqlens_padded.data_ptr(), n[0] - 1
@@ -96,6 +101,13 @@ def _heads(t: torch.Tensor, heads: int, head_dim: int, rows: int, what: str) -> 
     return ptr, stride if rows > 1 else heads * head_dim
 
 
+def _cache_strides(st: tuple, pages: int, page_size: int, heads: int, head_dim: int) -> tuple:
+    """An axis of one entry has no stride: any multiple of 8 does."""
+    return (st[0] if pages > 1 else page_size * heads * head_dim,
+            st[1] if page_size > 1 else max(head_dim, st[1] // 8 * 8),
+            st[2] if heads > 1 else head_dim, 1)
+
+
 def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor, heads: int, head_dim: int,
            B: int) -> tuple:
     shape = k_cache.shape
@@ -109,18 +121,15 @@ def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tens
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("k_cache, v_cache: the last axis must be contiguous")
 
-    def strides(st):  # an axis of one entry has no stride: any multiple of 8 does
-        return (st[0] if pages > 1 else page_size * heads * head_dim,
-                st[1] if page_size > 1 else max(head_dim, st[1] // 8 * 8),
-                st[2] if heads > 1 else head_dim)
-    ks = strides(ks)
-    if ks != strides(vs):
+    if pages == 1 or page_size == 1 or heads == 1:
+        ks, vs = (_cache_strides(st, pages, page_size, heads, head_dim) for st in (ks, vs))
+    if ks != vs:
         raise ValueError("k_cache and v_cache must have the same strides")
     ts, tt = block_table.shape, block_table.stride()
     if block_table.dtype is not torch.int32 or len(ts) != 2 or ts[0] != B or (ts[1] > 1 and tt[1] != 1):
         raise TypeError("block_table: expected an int32 CUDA tensor [num_seqs, max_pages], contiguous rows")
     table_stride = tt[0] if B > 1 else ts[1]
-    return (k_cache.data_ptr() or None, v_cache.data_ptr() or None, *ks, pages, page_size), \
+    return (k_cache.data_ptr() or None, v_cache.data_ptr() or None, ks[0], ks[1], ks[2], pages, page_size), \
         (block_table.data_ptr() or None, table_stride, ts[1])
 
 
