@@ -480,19 +480,21 @@ __global__ void __launch_bounds__(NShape<D>::kThreads) paged_narrow_kernel(const
     }
 }
 
-// The parts of the triples that several runs share, joined: one block per (row,
-// head), whose warps take the parts in turn (a single sequence's keys lie in
-// hundreds of parts: one token over 21,065 keys of 2 heads of 256 took 87 us
-// with one warp per row, 44 with four); rows of whole triples are done.
-template <int D>
+// The parts of the triples that several runs share, joined: W warps per (row,
+// head) take the parts in turn; rows of whole triples are done.  W is 4 where
+// there are few rows (a single sequence's keys lie in hundreds of parts: one
+// token over 21,065 keys of 2 heads of 256 took 87 us with one warp per row, 44
+// with four), and 1 where there are many, each with a few parts (48 requests of
+// 40 heads, back to back: 234 us against 292).
+template <int D, int W>
 __global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_constant__ PagedParams p, int tokens)
 {
-    constexpr int kWarps = 4;
-    __shared__ float s_acc[kWarps][D];
-    __shared__ float s_l[kWarps];
+    __shared__ float s_acc[W][W > 1 ? D : 1];
+    __shared__ float s_l[W];
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int v = (int)(blockIdx.x / (unsigned)p.num_q_heads), head = (int)(blockIdx.x - (unsigned)v * p.num_q_heads);
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W;
+    const long long task = (long long)blockIdx.x * (4 / W) + (threadIdx.x >> 5) / W;
+    const int v = (int)(task / p.num_q_heads), head = (int)(task - (long long)v * p.num_q_heads);
     // token `local` of sequence `seq`: of a mixed batch token v % tokens of
     // sequence v / tokens, else valid row v
     int seq = tokens > 0 ? v / tokens : -1, local = tokens > 0 ? v - seq * tokens : 0;
@@ -544,16 +546,16 @@ __global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_con
 #pragma unroll
     for (int e = 0; e < E; ++e)
         acc[e] = 0.f;
-    for (int c0 = b0 + warp; c0 <= b1; c0 += 32 * kWarps) {  // the warp's parts: every fourth
-        const int mine = c0 + lane * kWarps;
+    for (int c0 = b0 + warp; c0 <= b1; c0 += 32 * W) {  // the warp's parts: every W-th
+        const int mine = c0 + lane * W;
         const float2 ml = mine <= b1 ? p.part_ml[part_of(mine)] : make_float2(-INFINITY, 0.f);
         const float w = exp2f(ml.x - base);
         ll += w * ml.y;
-        const int count = min(32, (b1 - c0) / kWarps + 1);
+        const int count = min(32, (b1 - c0) / W + 1);
 #pragma unroll 8
         for (int i = 0; i < count; ++i) {
             const float f = __shfl_sync(0xffffffffu, w, i);
-            const float* from = p.part_o + part_of(c0 + i * kWarps) * D + lane * E;
+            const float* from = p.part_o + part_of(c0 + i * W) * D + lane * E;
 #pragma unroll
             for (int e = 0; e < E; e += 2) {
                 const float2 x = *reinterpret_cast<const float2*>(from + e);
@@ -563,21 +565,34 @@ __global__ void __launch_bounds__(128) paged_narrow_join_kernel(const __grid_con
         }
     }
     ll = group_sum<32>(ll);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        s_acc[warp][lane * E + e] = acc[e];
-    if (lane == 0)
-        s_l[warp] = ll;
-    __syncthreads();
-    ll = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-    const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
     const int64_t out_row = ls.row0 + local;
-    for (int c = threadIdx.x * 2; c < D; c += 2 * 32 * kWarps) {
-        const float x = (s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c]);
-        const float y = (s_acc[0][c + 1] + s_acc[1][c + 1]) + (s_acc[2][c + 1] + s_acc[3][c + 1]);
-        *reinterpret_cast<uint32_t*>(p.out + out_row * p.out_row_stride + head * D + c) = pack2(x * inv, y * inv);
+    uint16_t* out = p.out + out_row * p.out_row_stride + head * D;
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            s_acc[warp][lane * E + e] = acc[e];
+        if (lane == 0)
+            s_l[warp] = ll;
+        __syncthreads();  // W is the block's 4 warps: every one is here
+        if (warp != 0)
+            return;
+        ll = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            ll += s_l[w];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] += s_acc[w][lane * E + e];
+        }
     }
-    if (threadIdx.x == 0 && p.lse != nullptr)
+    const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+        *reinterpret_cast<uint32_t*>(out + lane * E + e) = pack2(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0 && p.lse != nullptr)
         p.lse[out_row * p.num_q_heads + head] = (mm + log2f(ll)) * kLn2;
 }
 
@@ -592,7 +607,9 @@ cudaError_t launch_n(const PagedParams& p, bool mixed, cudaStream_t stream)
         return e;
     const int tokens = mixed ? (kNarrowRows + p.group - 1) / p.group : 0;
     const long long rows = (mixed ? (long long)p.pk.num_seqs * tokens : p.pk.num_rows_padded) * p.num_q_heads;
-    return launch_kernel(paged_narrow_join_kernel<D>, dim3((unsigned)rows), 128, 0, stream, p, tokens);
+    if (rows <= 4 * 148)
+        return launch_kernel(paged_narrow_join_kernel<D, 4>, dim3((unsigned)rows), 128, 0, stream, p, tokens);
+    return launch_kernel(paged_narrow_join_kernel<D, 1>, dim3((unsigned)((rows + 3) / 4)), 128, 0, stream, p, tokens);
 }
 
 }  // namespace
