@@ -23,6 +23,20 @@ struct QueryTile {
     int kv_end;     // keys that the table can name (<= kv_len)
 };
 
+// Rows of sequence b's chunk: those that are valid and have a padded row; 0 for a
+// sequence that does not lie inside the buffer, which is skipped whole.  Every
+// kernel asks here, so that they agree on which rows exist.
+__device__ __forceinline__ int chunk_rows(const PagedParams& p, int b, int& ordinal0, int& row0)
+{
+    ordinal0 = __ldg(p.pk.cu_seqlens + b);
+    row0 = __ldg(p.pk.cu_seqlens_padded + b);
+    const int n = min(__ldg(p.pk.cu_seqlens + b + 1) - ordinal0, __ldg(p.pk.cu_seqlens_padded + b + 1) - row0);
+    if (row0 < 0 || ordinal0 < 0 || n <= 0 || (long long)row0 + n > p.pk.num_rows_padded ||
+        (long long)ordinal0 + n > p.pk.num_rows_padded)
+        return 0;
+    return n;
+}
+
 // Tile t of the batch, or false past the last one.  Warp-collective: 32
 // sequences per round, their tile counts summed by a shuffle scan.
 __device__ __forceinline__ bool map_query_tile(int t, const PagedParams& p, int R, int lane, QueryTile& q)
@@ -33,13 +47,7 @@ __device__ __forceinline__ bool map_query_tile(int t, const PagedParams& p, int 
         int n = 0, tiles = 0, c0 = 0, row0 = 0, kv = 0;
         if (b < p.pk.num_seqs) {
             kv = __ldg(p.kv_lens + b);
-            c0 = __ldg(p.pk.cu_seqlens + b);
-            row0 = __ldg(p.pk.cu_seqlens_padded + b);
-            n = min(__ldg(p.pk.cu_seqlens + b + 1) - c0, __ldg(p.pk.cu_seqlens_padded + b + 1) - row0);
-            // a sequence that does not lie inside the buffer is skipped
-            if (row0 < 0 || c0 < 0 || n <= 0 || (long long)row0 + n > p.pk.num_rows_padded ||
-                (long long)c0 + n > p.pk.num_rows_padded)
-                n = 0;
+            n = chunk_rows(p, b, c0, row0);
             tiles = (long long)n * p.group <= p.skip_rows ? 0 : (int)(((long long)n * p.group + R - 1) / R);
         }
         int sum = tiles;

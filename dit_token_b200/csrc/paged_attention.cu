@@ -292,8 +292,10 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     RowSlot s;
     if (!map_valid_row(v, p.pk.cu_seqlens, p.pk.cu_seqlens_padded, p.pk.num_seqs, p.pk.num_rows_padded, lane, s))
         return;
-    if ((long long)(__ldg(p.pk.cu_seqlens + s.seq + 1) - __ldg(p.pk.cu_seqlens + s.seq)) * p.group <= p.skip_rows)
-        return;  // the narrow kernel's
+    int ordinal0, row0;
+    const int n = chunk_rows(p, s.seq, ordinal0, row0);
+    if (s.local >= n || (long long)n * p.group <= p.skip_rows)
+        return;  // no block wrote its parts: skipped, or the narrow kernel's
     const int64_t part = partial_index(p, v, head, 0);
     float mm = -INFINITY;
     for (int i = lane; i < p.splits; i += 32)

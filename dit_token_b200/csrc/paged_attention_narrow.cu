@@ -68,14 +68,8 @@ __device__ __forceinline__ Listed list_seq(const PagedParams& p, int b)
     if (b >= p.pk.num_seqs)
         return s;
     s.kv_len = max(__ldg(p.kv_lens + b), 0);
-    s.ordinal0 = __ldg(p.pk.cu_seqlens + b);
-    s.row0 = __ldg(p.pk.cu_seqlens_padded + b);
-    s.n = min(__ldg(p.pk.cu_seqlens + b + 1) - s.ordinal0, __ldg(p.pk.cu_seqlens_padded + b + 1) - s.row0);
-    // a sequence that does not lie inside the buffer is skipped
-    if (s.row0 < 0 || s.ordinal0 < 0 || s.n <= 0 || (long long)s.row0 + s.n > p.pk.num_rows_padded ||
-        (long long)s.ordinal0 + s.n > p.pk.num_rows_padded)
-        return Listed{};
-    if ((long long)s.n * p.group > p.narrow_rows)
+    s.n = chunk_rows(p, b, s.ordinal0, s.row0);
+    if (s.n == 0 || (long long)s.n * p.group > p.narrow_rows)
         return Listed{};
     s.kv_end = (int)min((long long)s.kv_len, (long long)p.max_pages * p.page_size);
     s.q_tiles = (int)(((long long)s.n * p.group + kNRows - 1) / kNRows);

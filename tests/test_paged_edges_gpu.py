@@ -1,0 +1,59 @@
+"""The attention over a paged cache where its kernels have to agree with one
+another: malformed packings over a cut key axis."""
+import pytest
+import torch
+
+import dit_token_b200 as dit
+from _paged import Batch, check_attention, ints
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(x, cs, cp, rows, causal=True, window=0, **hints):
+    """dit_paged_attention over the first ``rows`` rows of the batch's buffer
+    with a packing of the test's own.  Outputs start as 7 and the workspace as
+    finite rubbish, so that what was not computed is seen."""
+    out = torch.full((x.rows, x.hq * x.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((x.rows, x.hq), 7.0, dtype=torch.float32, device="cuda")
+    hints.setdefault("max_chunk", max(x.chunks))
+    hints.setdefault("max_kv_len", max(x.kv))
+    nbytes = dit.dit_paged_attention_workspace(rows, len(x.chunks), **x.sizes(), **hints)
+    work = torch.full((nbytes,), 0x3f, dtype=torch.uint8, device="cuda")
+    dit.dit_paged_attention(x.q[:rows], x.k_cache, x.v_cache, x.table, x.kv_lens(), cs, cp, causal=causal,
+                            window=window, out=out[:rows], lse=lse[:rows], workspace=work, **x.sizes(), **hints)
+    return out, lse
+
+
+# Chunks and lengths whose key axis is cut, in pages that the tensor-memory
+# kernel takes (16) and that only the warp-level one does (10); more sequences
+# than a warp looks at in one round; a single token among the chunks.
+CUT = [([60, 300], [5000, 4000], 2), ([1, 60, 300], [700, 5000, 4000], 2), ([20] * 40, [2200] * 40, 1)]
+
+
+@pytest.mark.parametrize("page", [16, 10])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("chunks,pasts,hk", CUT)
+def test_a_sequence_past_the_buffer_is_skipped_whole(chunks, pasts, hk, d, page):
+    """The last sequence's final rows lie behind the buffer: none of its rows
+    is written, the others are as if it were not there."""
+    x = Batch(chunks, pasts, 2 * hk, hk, d, page=page, slack=0, seed=d + page).fill()
+    rows = x.first[-2] + chunks[-1] - 3
+    out, lse = attend(x, x.cs, x.cp, rows)
+    last = x.first[-2]
+    assert bool((out[last:] == 7).all()) and bool((lse[last:] == 7).all())
+    x.chunks = chunks[:-1] + [0]
+    check_attention(x, out, lse, True, 0)
+    assert bool((out[~x.valid()] == 7).all()) and bool((lse[~x.valid()] == 7).all())
+
+
+@pytest.mark.parametrize("page", [16, 10])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("slot", [8, 24])
+def test_a_slot_shorter_than_its_chunk(slot, d, page):
+    """A sequence of 40 valid rows in a padded slot of fewer: those that have a
+    padded row are its chunk, whichever kernel they fall to beside a chunk of
+    300 whose key axis is cut."""
+    x = Batch([slot, 300], [4000, 4000], 4, 2, d, page=page, slack=40, seed=slot + d).fill()
+    out, lse = attend(x, ints([0, 40, 340]), x.cp, x.rows, max_chunk=400)
+    check_attention(x, out, lse, True, 0)
+    assert bool((out[~x.valid()] == 7).all()) and bool((lse[~x.valid()] == 7).all())
