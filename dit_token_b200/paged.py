@@ -46,6 +46,16 @@ def _stream_on(index: int, stream) -> int:
     return int(stream)
 
 
+def _allocating_stream(index: int, on: int, stream) -> torch.cuda.Stream:
+    """The stream that owns what a call on ``stream`` (raw: ``on``) allocates.
+    Raw 0 and 1 are the default stream; torch.cuda.ExternalStream takes a 0 for
+    no stream given and hands out one of its own pool, on which memory would be
+    reused while the call still runs."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(on, device=index) if on > 1 else torch.cuda.default_stream(index)
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
@@ -291,7 +301,7 @@ def dit_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     if out is None or (workspace is None and rows > 0 and B > 0):
         # what is allocated here belongs to the stream that uses it
         with torch.cuda.device(dev), (contextlib.nullcontext() if stream is None else
-                                      torch.cuda.stream(torch.cuda.ExternalStream(on, device=dev))):
+                                      torch.cuda.stream(_allocating_stream(dev, on, stream))):
             if out is None:
                 out = torch.empty((rows, num_q_heads * head_dim), dtype=q.dtype, device=q.device)
             if workspace is None:
