@@ -40,7 +40,10 @@
 // that o(i) is complete and p(i) is free.
 //
 // Every wait is bounded: a wait that gives up raises a flag that ends the
-// block's other waits, and the block's rows become NaN.
+// block's other waits, and the block's rows become NaN.  Whatever gave up,
+// the fetching warps stay until their copies have landed and the issuing warp
+// until its products have ended (bounded too), so that neither writes to shared
+// or tensor memory that is no longer the block's.
 #include <cuda.h>
 
 #include "paged.cuh"
@@ -53,7 +56,14 @@ constexpr int kTcKeys = 128;   // keys per step
 constexpr int kTcThreads = 384;
 constexpr uint32_t kBlockBytes = kTcKeys * 128;  // 128 rows of 64 elements
 constexpr float kTcLag = 8.f;  // log2 of how far probabilities may pass 1
-constexpr long long kWaitCycles = 4000000000ll;  // a wait gives up after about two seconds
+constexpr long long kDrainCycles = 4000000000ll;  // about two seconds
+// DIT_STALL=1 at build time, for tests: each of the first four key heads has
+// barriers that never complete, and waits give up after a tenth of a millisecond
+// instead of two seconds.
+#ifndef DIT_STALL
+#define DIT_STALL 0
+#endif
+constexpr long long kWaitCycles = DIT_STALL ? 200000ll : kDrainCycles;
 
 // WHOLE: boxes of 8 rows of whole heads, else of 64 elements.  (A template:
 // with strides read at run time the issuing warp fell behind, 2355 -> 2473 us
@@ -108,6 +118,14 @@ __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, vo
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort)
 {
     return mbar_try(bar, parity) || mbar_wait_long(bar, parity, abort);
+}
+
+// Until the phase is over, whether or not the block has given up.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity)
+{
+    const long long from = clock64();
+    while (!mbar_try(bar, parity) && clock64() - from < kDrainCycles) {
+    }
 }
 
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
@@ -305,16 +323,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     if (tid == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
+        auto never = [&](int head) { return DIT_STALL && kvh == head ? 1u : 0u; };  // one arrival too many asked for
         for (int s = 0; s < NS; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+            mbar_init(empty(s), 1 + never(1));
         }
-        mbar_init(q_full, S::kTiles * kTcRows);
+        mbar_init(q_full, S::kTiles * kTcRows + never(0));
         for (int t = 0; t < 2; ++t) {
             mbar_init(s_full(t), 1);
             mbar_init(p_full(t, 0), 4);
-            mbar_init(p_full(t, 1), 4);
-            mbar_init(o_full(t), 1);
+            mbar_init(p_full(t, 1), 4 + never(2));
+            mbar_init(o_full(t), 1 + never(3));
         }
         mbar_init(drained, 1);
         mbar_init(clean, 1);
@@ -445,11 +464,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 if (go && i + 1 < steps)
                     commit(empty(ks));
             }
-            if (!go && steps > 0) {  // given up: let what was issued end before the memory is freed
+            if (steps > 0) {  // what was issued ends before the memory is freed
                 commit(drained);
-                const long long from = clock64();
-                while (!mbar_try(drained, 0) && clock64() - from < kWaitCycles) {
-                }
+                mbar_drain(drained, 0);
                 __syncwarp();
             }
         } else if (warp < 11) {
@@ -517,14 +534,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                         mbar_arrive(clean);
                 }
             }
-            // given up: let the copies under way land before the block ends
-            if (i < steps && lane == 0) {
-                const long long from = clock64();
-                for (int e = max(i - NS / 2, 0); e < i; ++e) {
-                    const int j = 2 * e + of_v;
-                    while (!mbar_try(full(j % NS), (uint32_t)(j / NS) & 1u) && clock64() - from < kWaitCycles) {
-                    }
-                }
+            // the copies under way land before the block ends
+            for (int e = max(i - NS / 2, 0); lane == 0 && e < i; ++e) {
+                const int j = 2 * e + of_v;
+                mbar_drain(full(j % NS), (uint32_t)(j / NS) & 1u);
             }
         }
     } else {
