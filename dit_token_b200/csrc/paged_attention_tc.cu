@@ -635,6 +635,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             go = __all_sync(0xffffffffu, go);
             tc_fence_after();
         }
+        if (!go)
+            m = NAN;  // and with it lse, or the split's weight in the join
         // the thread's row: output, or the split's part
         const bool whole = p.splits == 1;
         const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         }
         if (mine) {
             if (!whole)
-                p.part_ml[part] = make_float2(n1 > n0 ? (go ? m : NAN) : -INFINITY, l);
+                p.part_ml[part] = make_float2(n1 > n0 ? m : -INFINITY, l);
             else if (p.lse != nullptr)
                 p.lse[(int64_t)(q.row0 + token) * p.num_q_heads + head] = (m + log2f(l)) * kLn2;
         }

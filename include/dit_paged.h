@@ -146,6 +146,9 @@ DIT_API dit_status dit_qkv_rope_append(const void* q, int64_t q_row_stride, cons
  * The slots of tokens >= kv_lens[b] may hold anything; the cached tokens
  * below kv_lens[b] must be finite, also those a mask hides from some of the
  * queries (a hidden value is multiplied by 0).
+ * A chunk kernel whose copies or products do not end within about two seconds
+ * (a device fault) gives up: the rows it was computing become NaN in out and in
+ * lse; the call itself has returned by then.
  * The result does not depend on what else is in the batch's buffers, and is
  * bitwise reproducible for the same call.
  *

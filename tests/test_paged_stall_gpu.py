@@ -54,3 +54,7 @@ def run(lib, lse="pass"):
 
 def test_rows_of_a_block_that_gave_up_are_nan(stalling):
     run(stalling)
+
+
+def test_so_is_their_lse(stalling):
+    run(stalling, lse='assert bool(lse[ok][:, :8].isnan().all()), "lse of a row of a head that gave up"')
