@@ -623,6 +623,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 tc_tie32(again);
                 tc_tie32(again + 32);
                 mask_and_top(again, clear, r_lo - k0, r_hi - k0);
+                tc_wait_st();  // two stores to the same columns keep no order of their own
                 part = exponentials(again, p.scale_log2, base_m, p_at);
             }
             hand_over(p_full(t, 0));

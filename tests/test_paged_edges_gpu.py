@@ -57,3 +57,27 @@ def test_a_slot_shorter_than_its_chunk(slot, d, page):
     out, lse = attend(x, ints([0, 40, 340]), x.cp, x.rows, max_chunk=400)
     check_attention(x, out, lse, True, 0)
     assert bool((out[~x.valid()] == 7).all()) and bool((lse[~x.valid()] == 7).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_maxima_that_grow_at_every_step(d, sign):
+    """Every step of 128 keys tops the ones before it by more than the running
+    maximum may lag (2^8), for some rows (and falls for others, whose queries
+    are negative), so probabilities are computed against an old maximum first
+    and then again: 30 calls agree bit for bit and with the definition."""
+    x = Batch([300], [2500], 4, 2, d, seed=d).fill()
+    where = x.place(0, 0, x.kv[0])
+    step = (torch.arange(x.kv[0], device="cuda") // 128).float()
+    # 20 per step in the exponent's powers of two; the noise in the keys stays
+    x.k_cache[where] = (x.k_cache[where].float() + (step * 14.0)[:, None, None] / d ** 0.5).bfloat16()
+    x.q[:300] = 1.0
+    x.q[1:300:3] = -1.0
+    x.q[:300] *= sign
+    first = None
+    for keys in [0] * 10 + [1] * 10 + [max(x.kv)] * 10:  # cut and whole key axes
+        out, lse = attend(x, x.cs, x.cp, x.rows, max_kv_len=keys or x.max_pages * x.page)
+        if first is None or keys != first[2]:
+            check_attention(x, out, lse, True, 0)
+            first = (out, lse, keys)
+        assert torch.equal(out[x.valid()], first[0][x.valid()]) and torch.equal(lse[x.valid()], first[1][x.valid()])
