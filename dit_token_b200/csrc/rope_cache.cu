@@ -98,8 +98,8 @@ __device__ __forceinline__ void pair_regs(int e, int& a, int& z)
 }
 
 template <int MODE, bool NORM>
-__device__ __forceinline__ void fold(PairCoef& pc, const float (&c)[4], const float (&s)[4], const uint16_t* w, int o0,
-                                     int o1)
+__device__ __forceinline__ void fold(PairCoef& pc, const float (&c)[4], const float (&s)[4], bool turns,
+                                     const uint16_t* w, int o0, int o1)
 {
     float wf[8];
     if (NORM) {
@@ -113,8 +113,8 @@ __device__ __forceinline__ void fold(PairCoef& pc, const float (&c)[4], const fl
         pair_regs<MODE>(e, a, z);
         const float wa = NORM ? wf[a] : 1.f, wz = NORM ? wf[z] : 1.f;
         pc.c0[e] = wa * c[e];
-        pc.c1[e] = -wz * s[e];
-        pc.c2[e] = wa * s[e];
+        pc.c1[e] = turns ? -wz * s[e] : 0.f;
+        pc.c2[e] = turns ? wa * s[e] : 0.f;
         pc.c3[e] = wz * c[e];
     }
 }
@@ -145,7 +145,11 @@ __device__ __forceinline__ void turn_batch(uint16_t* to, int64_t step, int heads
         for (int e = 0; e < 4; ++e) {
             int a, z;
             pair_regs<MODE>(e, a, z);
-            const float oa = fmaf(v[z], pc.c1[e], v[a] * pc.c0[e]), oz = fmaf(v[z], pc.c3[e], v[a] * pc.c2[e]);
+            // What passes has no part in its neighbour: 0 times an infinite one
+            // would not be 0.  (Two selects per pair, 1 % of the long video's time;
+            // a branch where r is 0, as an infinite element makes it, took 2 %.)
+            const float va = NORM && !turns ? 0.f : v[a], vz = NORM && !turns ? 0.f : v[z];
+            const float oa = fmaf(vz, pc.c1[e], v[a] * pc.c0[e]), oz = fmaf(v[z], pc.c3[e], va * pc.c2[e]);
             o[a] = NORM ? r * oa : oa;
             o[z] = NORM ? r * oz : oz;
         }
@@ -238,9 +242,9 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
         }
     }
     PairCoef pq, pk;
-    fold<MODE, NORM>(pq, c, sn, p.q_weight, o0, o1);
+    fold<MODE, NORM>(pq, c, sn, turns, p.q_weight, o0, o1);
     if (NORM)
-        fold<MODE, NORM>(pk, c, sn, p.k_weight, o0, o1);
+        fold<MODE, NORM>(pk, c, sn, turns, p.k_weight, o0, o1);
 
     for (int b = b0; b < b1; ++b) {
         uint4 nxt[U];
