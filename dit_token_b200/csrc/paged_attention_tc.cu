@@ -23,6 +23,8 @@
 //                   last step's rows of v behind the block's keys: the cache may
 //                   hold anything behind the last token, and 0 * NaN must not
 //                   reach the sums
+//   warp 11         writes zeros over the first step's rows of v that lie before
+//                   every row's window, whose tokens may be gone
 // A box costs its warp some 40 cycles, whatever it holds.  (Heads of 256 in
 // pages of 40: 154 us in boxes of 64 elements, 92 in whole heads, 81 by two
 // warps; the video chunk in pages of 100, boxes of 4 rows: 5936 us by one warp,
@@ -78,7 +80,7 @@ struct TcShape {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kRing = kTiles * kTile;
     static constexpr uint32_t kBars = kRing + kSlots * kTile;
-    static constexpr int kNumBars = 2 * kSlots + 11;
+    static constexpr int kNumBars = 2 * kSlots + 12;
     static constexpr uint32_t kTmemPtr = kBars + kNumBars * 8;
     static constexpr uint32_t kAbort = kTmemPtr + 4;
     static constexpr uint32_t kSmem = kAbort + 4;
@@ -319,6 +321,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     auto o_full = [&](int t) { return bars + 8u * (2 * NS + 3 + t); };
     auto p_full = [&](int t, int h) { return bars + 8u * (2 * NS + 5 + 2 * t + h); };
     const uint32_t drained = bars + 8u * (2 * NS + 9), clean = bars + 8u * (2 * NS + 10);
+    const uint32_t clean_first = bars + 8u * (2 * NS + 11);
 
     if (tid == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
@@ -337,6 +340,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         }
         mbar_init(drained, 1);
         mbar_init(clean, 1);
+        mbar_init(clean_first, 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         proxy_fence();
@@ -384,6 +388,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     // the last step's first row behind the block's keys: not fetched, or not
     // of a token; zeroed
     const int behind = min(k_hi - (k_lo + (steps - 1) * kTcKeys), kTcKeys);
+    // the first step's rows that no row of the block sees; zeroed
+    const int before = max(lo[0] - k_lo, 0);
+    // by a whole warp, behind the copies into the slot
+    auto zero_rows_of_v = [&](int slot, int from, int to, uint32_t bar) {
+        for (int c = 0; c < D / 64; ++c)
+            for (int e = from * 8 + lane; e < to * 8; e += 32) {
+                const int r = e >> 3;
+                *reinterpret_cast<uint4*>(smem + S::kRing + slot * S::kTile + c * S::kBlock + (r >> 3) * S::kGroup +
+                                          (r & 7) * 128 + (e & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar);
+    };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -435,6 +454,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                     if (in(t, 0))
                         scores(t, 0);
                 commit(empty(0));
+                go = before == 0 || wait(clean_first, 0);
             }
             for (int i = 0; go && i < steps; ++i) {
                 const int vt = 2 * i + 1, kt = 2 * i + 2;
@@ -520,25 +540,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
             // so the parity it waits for is the tile's own.
             if (of_v && i == steps && behind < kTcKeys && steps > 0) {
                 const int j = 2 * steps - 1, slot = j % NS;
-                if (__all_sync(0xffffffffu, mbar_wait(full(slot), (uint32_t)(j / NS) & 1u, abort))) {
-                    for (int c = 0; c < D / 64; ++c)
-                        for (int e = behind * 8 + lane; e < kTcKeys * 8; e += 32) {
-                            const int r = e >> 3;
-                            *reinterpret_cast<uint4*>(smem + S::kRing + slot * S::kTile + c * S::kBlock +
-                                                      (r >> 3) * S::kGroup + (r & 7) * 128 + (e & 7) * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    proxy_fence();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(clean);
-                }
+                if (__all_sync(0xffffffffu, mbar_wait(full(slot), (uint32_t)(j / NS) & 1u, abort)))
+                    zero_rows_of_v(slot, behind, kTcKeys, clean);
             }
             // the copies under way land before the block ends
             for (int e = max(i - NS / 2, 0); lane == 0 && e < i; ++e) {
                 const int j = 2 * e + of_v;
                 mbar_drain(full(j % NS), (uint32_t)(j / NS) & 1u);
             }
+        } else if (steps > 0 && before > 0) {
+            // v's first tile is the second one fetched; its slot is not used
+            // again before its product, which waits for this
+            if (__all_sync(0xffffffffu, mbar_wait(full(1), 0, abort)))
+                zero_rows_of_v(1, 0, before, clean_first);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");

@@ -143,9 +143,11 @@ DIT_API dit_status dit_qkv_rope_append(const void* q, int64_t q_row_stride, cons
  * A query that sees nothing (kv_lens[b] < n, or 0) gives o = 0, lse = -inf.
  * Scores, softmax and sums are fp32; the probabilities are rounded to bf16
  * for their product with v, and o once more to bf16.
- * The slots of tokens >= kv_lens[b] may hold anything; the cached tokens
- * below kv_lens[b] must be finite, also those a mask hides from some of the
- * queries (a hidden value is multiplied by 0).
+ * The slots of tokens >= kv_lens[b] may hold anything, and so may those of
+ * tokens that lie before every query's window (their pages may be given
+ * away, their table entries be stale or none).  The other cached tokens must be
+ * finite, also those a mask hides from some of the queries (a hidden value is
+ * multiplied by 0).
  * A chunk kernel whose copies or products do not end within about two seconds
  * (a device fault) gives up: the rows it was computing become NaN in out and in
  * lse; the call itself has returned by then.

@@ -1,5 +1,7 @@
 """The attention over a paged cache where its kernels have to agree with one
 another: malformed packings over a cut key axis."""
+import math
+
 import pytest
 import torch
 
@@ -81,3 +83,29 @@ def test_maxima_that_grow_at_every_step(d, sign):
             check_attention(x, out, lse, True, 0)
             first = (out, lse, keys)
         assert torch.equal(out[x.valid()], first[0][x.valid()]) and torch.equal(lse[x.valid()], first[1][x.valid()])
+
+
+@pytest.mark.parametrize("page", [16, 10])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [1, 50, 127, 128, 129, 700])
+def test_tokens_behind_every_window_may_hold_anything(window, causal, d, page):
+    """A token that no query of its sequence's chunk sees (its page may have
+    been given away) is NaN in the cache or has no page at all: the outputs are
+    those over the other tokens, whole key axes and cut ones, chunks and single
+    tokens."""
+    chunks, pasts = [140, 1, 33], [1500, 900, 2100]
+    x = Batch(chunks, pasts, 4, 2, d, page=page, seed=window).fill()
+    want, expired = x.table.clone(), [max(0, p - window + 1) for p in pasts]
+    for b, n in enumerate(expired):
+        where = x.place(b, 0, n)
+        x.k_cache[where], x.v_cache[where] = math.nan, math.nan
+        x.table[b, :n // page // 2] = -7
+    outs = [attend(x, x.cs, x.cp, x.rows, causal, window, max_kv_len=keys)
+            for keys in (1, max(x.kv), x.max_pages * page)]
+    x.table = want
+    for b, n in enumerate(expired):  # the definition multiplies them by 0 as well: finite for it
+        where = x.place(b, 0, n)
+        x.k_cache[where], x.v_cache[where] = 0.0, 0.0
+    for out, lse in outs:
+        check_attention(x, out, lse, causal, window)
