@@ -18,6 +18,7 @@
 // the warp-level matrix instructions and what feeds them: 163 TFLOP/s on the
 // video chunk (2.74 TFLOP in 16.8 ms, 4,132 rows over 32,360 keys, 40 heads).
 #include "paged_mma.cuh"
+#include "paged_splits.h"
 
 namespace dit {
 namespace {
@@ -394,20 +395,21 @@ bool paged_plan(int64_t rows, int num_seqs, int num_q_heads, int num_kv_heads, i
     int64_t keys = max_kv_len;
     if (window > 0 && window + plan.tile_rows < keys)
         keys = window + plan.tile_rows;
-    const int64_t full = rows * group / plan.tile_rows;
-    const int64_t blocks = (full > num_seqs ? full : num_seqs) * num_kv_heads;
     int64_t splits;
     if (plan.kind == kPagedTc) {
-        // One block per SM.  Splits only fill SMs that would have no block:
-        // each costs its block's start and end (about 9 us, four steps) and the
-        // write and read of its part (a chunk of 1,000 rows of 40 heads over
-        // itself: 59 us whole, 185 in 4 splits), so runs are 512 keys at least.
-        splits = 160 / blocks;
-        const int64_t most = keys / 512;
-        splits = splits < most ? splits : most;
+        // Tiles the batch is expected to have: chunks that are all as long as the
+        // longest, or ragged ones whose last tiles are half full on the average.
+        const int64_t longest = num_seqs * ((chunk * group + plan.tile_rows - 1) / plan.tile_rows);
+        int64_t expected = rows * group / plan.tile_rows + (num_seqs + 1) / 2;
+        expected = expected > num_seqs ? expected : num_seqs;
+        if (expected > longest || num_seqs * chunk <= rows)
+            expected = longest;
+        splits = tc_splits(expected * num_kv_heads, keys, part);
     } else {
         // several short blocks per SM: enough of them for the GPU several times
         // over, no run shorter than 128 keys
+        const int64_t full = rows * group / plan.tile_rows;
+        const int64_t blocks = (full > num_seqs ? full : num_seqs) * num_kv_heads;
         splits = (148 * 8 + blocks - 1) / blocks;
         const int64_t most = (keys + 127) / 128;
         splits = splits < most ? splits : most;
