@@ -24,6 +24,8 @@
 #include "launch.h"
 #include "rope.cuh"
 
+#include <type_traits>
+
 namespace dit {
 namespace {
 
@@ -113,8 +115,8 @@ __device__ __forceinline__ void fold(PairCoef& pc, const float (&c)[4], const fl
         pair_regs<MODE>(e, a, z);
         const float wa = NORM ? wf[a] : 1.f, wz = NORM ? wf[z] : 1.f;
         pc.c0[e] = wa * c[e];
-        pc.c1[e] = turns ? -wz * s[e] : 0.f;
-        pc.c2[e] = turns ? wa * s[e] : 0.f;
+        pc.c1[e] = NORM && !turns ? 0.f : -wz * s[e];
+        pc.c2[e] = NORM && !turns ? 0.f : wa * s[e];
         pc.c3[e] = wz * c[e];
     }
 }
@@ -146,8 +148,8 @@ __device__ __forceinline__ void turn_batch(uint16_t* to, int64_t step, int heads
             int a, z;
             pair_regs<MODE>(e, a, z);
             // What passes has no part in its neighbour: 0 times an infinite one
-            // would not be 0.  (Two selects per pair, 1 % of the long video's time;
-            // a branch where r is 0, as an infinite element makes it, took 2 %.)
+            // would not be 0.  (Two selects per pair, 1 % of the ragged prompts'
+            // time; a branch where r is 0, as an infinite element makes it, 2 %.)
             const float va = NORM && !turns ? 0.f : v[a], vz = NORM && !turns ? 0.f : v[z];
             const float oa = fmaf(vz, pc.c1[e], v[a] * pc.c0[e]), oz = fmaf(v[z], pc.c3[e], va * pc.c2[e]);
             o[a] = NORM ? r * oa : oa;
@@ -161,7 +163,10 @@ __device__ __forceinline__ void turn_batch(uint16_t* to, int64_t step, int heads
     }
 }
 
-template <int D, int MODE, bool NORM, bool APPEND, int U>
+// PART: only the first rotary_dim elements of a head turn (or none), else all do,
+// and nothing is asked of a lane (the long video 176 us with the question, 172
+// without; it costs nothing where there are no weights).
+template <int D, int MODE, bool NORM, bool APPEND, int U, bool PART>
 __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __grid_constant__ RopeCacheParams p)
 {
     constexpr int LPH = D / 8;          // lanes per head
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
     const int b0 = run * p.batches_per_run, b1 = min(b0 + p.batches_per_run, total);
     if (b0 >= b1)
         return;
-    const bool turns = li < (p.rotary_dim >> 3);
+    const bool turns = !PART || li < (p.rotary_dim >> 3);
     const int half = p.rotary_dim >> 1;
     const int o0 = quad_off<MODE>(li, 0, turns, half), o1 = quad_off<MODE>(li, 1, turns, half);
 
@@ -273,6 +278,13 @@ __global__ void __launch_bounds__(kRcWarps * kWarp) rope_cache_kernel(const __gr
     }
 }
 
+// A runtime choice as a compile-time one.
+template <typename F>
+cudaError_t with_bool(bool b, F f)
+{
+    return b ? f(std::true_type{}) : f(std::false_type{});
+}
+
 template <int D, int U>
 cudaError_t launch_rc(RopeCacheParams p, int mode, cudaStream_t stream)
 {
@@ -288,16 +300,17 @@ cudaError_t launch_rc(RopeCacheParams p, int mode, cudaStream_t stream)
     const unsigned grid = (unsigned)(((long long)p.pk.num_rows_padded * p.runs_per_row + kRcWarps - 1) / kRcWarps);
     const bool norm = p.k_weight != nullptr;
     auto launch = [&](auto* kernel) { return launch_kernel(kernel, grid, kRcWarps * kWarp, 0, stream, p); };
-    const bool half = mode == kRopeHalf, append = p.block_table != nullptr;
-    if (half && norm)
-        return append ? launch(rope_cache_kernel<D, kRopeHalf, true, true, U>) : launch(rope_cache_kernel<D, kRopeHalf, true, false, U>);
-    if (half)
-        return append ? launch(rope_cache_kernel<D, kRopeHalf, false, true, U>) : launch(rope_cache_kernel<D, kRopeHalf, false, false, U>);
-    if (norm)
-        return append ? launch(rope_cache_kernel<D, kRopeInterleaved, true, true, U>)
-                      : launch(rope_cache_kernel<D, kRopeInterleaved, true, false, U>);
-    return append ? launch(rope_cache_kernel<D, kRopeInterleaved, false, true, U>)
-                  : launch(rope_cache_kernel<D, kRopeInterleaved, false, false, U>);
+    auto pick = [&](auto norm_, auto append_, auto half_, auto part_) {
+        constexpr bool kNorm = decltype(norm_)::value, kPart = !kNorm || decltype(part_)::value;
+        constexpr int kMode = decltype(half_)::value ? kRopeHalf : kRopeInterleaved;
+        return launch(rope_cache_kernel<D, kMode, kNorm, decltype(append_)::value, U, kPart>);
+    };
+    const bool half = mode == kRopeHalf, append = p.block_table != nullptr, part = p.rotary_dim < D;
+    return with_bool(norm, [&](auto n) {
+        return with_bool(append, [&](auto a) {
+            return with_bool(half, [&](auto h) { return with_bool(part, [&](auto t) { return pick(n, a, h, t); }); });
+        });
+    });
 }
 
 // Steps per batch: 4, or 1 where 4-step batches would leave over half of their
