@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
     auto o_full = [&](int t) { return bars + 8u * (2 * NS + 3 + t); };
     auto p_full = [&](int t, int h) { return bars + 8u * (2 * NS + 5 + 2 * t + h); };
     const uint32_t drained = bars + 8u * (2 * NS + 9), clean = bars + 8u * (2 * NS + 10);
-    const uint32_t clean_first = bars + 8u * (2 * NS + 11);
+    const uint32_t first_landed = bars + 8u * (2 * NS + 11);
 
     if (tid == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
         }
         mbar_init(drained, 1);
         mbar_init(clean, 1);
-        mbar_init(clean_first, 1);
+        mbar_init(first_landed, 1);
         *abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         proxy_fence();
@@ -454,7 +454,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                     if (in(t, 0))
                         scores(t, 0);
                 commit(empty(0));
-                go = before == 0 || wait(clean_first, 0);
             }
             for (int i = 0; go && i < steps; ++i) {
                 const int vt = 2 * i + 1, kt = 2 * i + 2;
@@ -520,18 +519,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                     look_up(i + 1);
                 if (j >= NS && !__all_sync(0xffffffffu, mbar_wait(empty(slot), (uint32_t)(j / NS - 1) & 1u, abort)))
                     break;
+                // a first tile that warp 11 has to look at reports to it
+                const uint32_t bar = of_v && i == 0 && before > 0 ? first_landed : full(slot);
                 const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, there));
                 if (lane == 0)
-                    mbar_expect(full(slot), boxes * (uint32_t)box * (D * 2));
+                    mbar_expect(bar, boxes * (uint32_t)box * (D * 2));
                 __syncwarp();
                 if (there) {
                     const uint32_t to = base + S::kRing + slot * S::kTile + (uint32_t)lane * (WHOLE ? S::kGroup : (uint32_t)box * 128);
                     if (WHOLE) {
-                        tma_box3(to, map, row, x / 64, full(slot));
+                        tma_box3(to, map, row, x / 64, bar);
                     } else {
 #pragma unroll
                         for (int c = 0; c < D / 64; ++c)
-                            tma_box(to + c * kBlockBytes, map, x + 64 * c, row, full(slot));
+                            tma_box(to + c * kBlockBytes, map, x + 64 * c, row, bar);
                     }
                 }
                 __syncwarp();
@@ -549,10 +550,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_attention_tc_kernel(const
                 mbar_drain(full(j % NS), (uint32_t)(j / NS) & 1u);
             }
         } else if (steps > 0 && before > 0) {
-            // v's first tile is the second one fetched; its slot is not used
-            // again before its product, which waits for this
-            if (__all_sync(0xffffffffu, mbar_wait(full(1), 0, abort)))
-                zero_rows_of_v(1, 0, before, clean_first);
+            // v's first tile, the second one fetched; behind this it counts as there
+            mbar_drain(first_landed, 0);
+            __syncwarp();
+            zero_rows_of_v(1, 0, before, full(1));
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
