@@ -28,7 +28,7 @@
 // A box costs its warp some 40 cycles, whatever it holds.  (Heads of 256 in
 // pages of 40: 154 us in boxes of 64 elements, 92 in whole heads, 81 by two
 // warps; the video chunk in pages of 100, boxes of 4 rows: 5936 us by one warp,
-// 3252 by two.)
+// 3224 by two.)
 // The softmax warps first copy q.  (Fetching k and v with 16-byte asynchronous
 // copies by three warps held the video chunk at 3584 us, 2.8 us a step, and
 // gathering TMA copies of four rows at 6210; without any copies it took 2611.)

@@ -17,9 +17,10 @@
 // GPU with whole rows: its rows' batches are spread over up to as many warps,
 // which repeats the angles and shortens the chain of loads (launch_rc).  q, k
 // and v are batched apart, so a batch has one weight vector and one
-// destination.  Measured: 61,888 rows of 16 + 16 heads of 128 in 162 us (6.27
-// TB/s), four ragged prompts of 53,619 rows of 40 + 8 heads in 223 us (5.90),
-// 20,819 rows of 40 + 8 + 8 heads into pages of 16 in 97.5 us (6.12).
+// destination.  Measured among other passes (behind an L2 that holds nothing to
+// write back): 61,888 rows of 16 + 16 heads of 128 in 168 us, 6.0 TB/s (161),
+// four ragged prompts of 53,619 rows of 40 + 8 heads in 239 us, 5.5 (225), 20,819
+// rows of 40 + 8 + 8 heads into pages of 16 in 103 us, 5.8 (97.5).
 #include "common.cuh"
 #include "launch.h"
 #include "rope.cuh"
@@ -81,13 +82,12 @@ __device__ __forceinline__ void store_quads(uint16_t* head, int o0, int o1, uint
 // What a pair's elements are multiplied by: with weights these are folded into
 // the rotation, (o_a, o_b) = r (x_a c0 + x_b c1, x_a c2 + x_b c3), so that a
 // normed and turned pair costs two products, two fused ones and r.  A lane that
-// passes has c0 = w_a, c3 = w_b and zeros.  (Weights applied on their own: 186
-// us for the long video.)  q's and k's coefficients are both kept: registers
-// decide how many warps hide the loads, and with a head's stride known (D) for
-// all but the cache's writes they fit in 96 (162 us, 97 % of the measured copy
-// rate; in one kernel for both destinations 126 registers and 197 us, one set
-// folded again between q and k 174).  Without weights there is one set: 150 us
-// for the same bytes.
+// passes has c0 = w_a, c3 = w_b and zeros.  q's and k's coefficients are both
+// kept: registers decide how many warps hide the loads, and with a head's stride
+// known (D) for all but the cache's writes they fit in 96.  The long video, single
+// calls behind a clean L2: 161 us; weights applied on their own 186, one kernel
+// for both destinations (126 registers) 197, one set folded again between q and k
+// 174, without weights (one set) 154.
 struct PairCoef {
     float c0[4], c1[4], c2[4], c3[4];
 };
